@@ -26,6 +26,8 @@ MOE_MEGA_STATE_BYTES = 144 << 10  # its workspace state region (offset 0), zero 
 MOE_MEGA_ERR_WORD = 800           # uint64 word of that region that a wait which gave up sets
 MOE_MEGA_HCOUNT_WORD = 816        # first per-expert h count of that region (words hcount + e)
 
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_SQRTSOFTPLUS = 0, 1, 2
+
 # Every symbol include/moe_w4a4.h declares.
 EXPORTED = (
     "moe_w4a4_query",
@@ -39,6 +41,11 @@ EXPORTED = (
     "moe_w4a4_status_string",
     "moe_w4a4_workspace_layout",
     "moe_w4a4_run_stages",
+    "moe_w4a4_add_rmsnorm",
+    "moe_w4a4_router",
+    "moe_w4a4_linear_query",
+    "moe_w4a4_linear_prepare",
+    "moe_w4a4_linear",
 )
 
 
@@ -51,6 +58,10 @@ class MoeError(RuntimeError):
 class moe_w4a4_cfg(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "hidden", "inter", "num_experts", "topk", "max_tokens", "group_size", "mma_type", "activation")]
+
+
+class moe_w4a4_linear_cfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_features", "out_features", "max_tokens", "mma_type")]
 
 
 class moe_w4a4_ws_layout(ctypes.Structure):
@@ -86,6 +97,13 @@ _lib.moe_w4a4_status_string.argtypes = [ctypes.c_int]
 _lib.moe_w4a4_status_string.restype = ctypes.c_char_p
 _lib.moe_w4a4_workspace_layout.argtypes = [_CFG, ctypes.POINTER(moe_w4a4_ws_layout)]
 _lib.moe_w4a4_run_stages.argtypes = [_CFG, _P, _i32, _P, _P, _P, _P, _P, _sz, ctypes.c_uint32, _P, _P]
+_f32, _i64 = ctypes.c_float, ctypes.c_int64
+_LCFG = ctypes.POINTER(moe_w4a4_linear_cfg)
+_lib.moe_w4a4_add_rmsnorm.argtypes = [_i32, _i32, _i32, _i64, _i32, _P, _P, _P, _f32, _f32, _P, _P, _P, _P, _P]
+_lib.moe_w4a4_router.argtypes = [_i32, _i32, _i64, _i32, _i32, _i32, _i32, _P, _P, _i32, _f32, _P, _P, _P]
+_lib.moe_w4a4_linear_query.argtypes = [_LCFG, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]
+_lib.moe_w4a4_linear_prepare.argtypes = [_LCFG, _P, _P, _P, _sz, _P]
+_lib.moe_w4a4_linear.argtypes = [_LCFG, _P, _i32, _P, _P, _P, _P, _i32, _P, _P, _sz, _P]
 for _n in EXPORTED:
     if _n != "moe_w4a4_status_string":
         getattr(_lib, _n).restype = ctypes.c_int
@@ -296,3 +314,150 @@ def moe_w4a4_run_stages(cfg, prepared, num_tokens: int, x, topk_ids, topk_weight
                                     _ptr(topk_weights), _ptr(out), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), int(stages), _ptr(gemm1_acc),
                                     _stream(stream)), "moe_w4a4_run_stages")
+
+
+# ---- operators around the layer ----------------------------------------------
+# These calls are a few microseconds of GPU work, so their checks go straight to
+# the tensors' properties; the rules are _expect's.
+
+def _raw_stream(stream, device_index: int) -> int:
+    return int(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(device_index)
+
+
+def _fits(t, name: str, dtypes, shape, device_index: int) -> int:
+    """Device address of a contiguous tensor of one of the dtypes, of that
+    shape, on device `device_index`; else ValueError."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor, got one on {t.device}")
+    if t.device.index != device_index:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device_index}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+_BF16 = (torch.bfloat16,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+_U8, _F32, _I32 = (torch.uint8,), (torch.float32,), (torch.int32,)
+
+
+def _device_of(t, name: str) -> int:
+    """Index of the current device, on which t has to be."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor, got one on {t.device}")
+    return torch.cuda.current_device()
+
+
+def moe_w4a4_add_rmsnorm(x, residual, weight, eps: float, residual_out=None, y=None, codes=None, scales=None,
+                         mma_type: int = MOE_MMA_MXF4_X_MXF4, tensor_scale: float = 1.0, stream=None) -> None:
+    """h = x + residual (or x), into residual_out; y = h * weight / rms(h) in
+    bf16; codes and scales = y quantized as mma_type's activations (NVFP4 under
+    tensor_scale).  x bf16 [rows, cols]; residual None, or bf16 / float32 [rows,
+    cols]; weight bf16 / float32 [cols]; residual_out like residual (may be it;
+    None exactly when residual is None); y None or bf16 [rows, cols] (may be x);
+    codes and scales both None, or uint8 [rows, cols/2] (E4M3: cols) and
+    [rows, cols/32] (NVFP4: cols/16)."""
+    dev = _device_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [rows, cols], got shape {tuple(x.shape)}")
+    rows, cols = shape = x.shape
+    px = _fits(x, "x", _BF16, shape, dev)
+    pw = _fits(weight, "weight", _BF16_F32, (cols,), dev)
+    pr = pro = py = pc = ps = None
+    res_dtype = 0
+    if residual is not None:
+        pr = _fits(residual, "residual", _BF16_F32, shape, dev)
+        if residual_out is None:
+            raise ValueError("residual_out: needed with a residual")
+        pro = _fits(residual_out, "residual_out", (residual.dtype,), shape, dev)
+        res_dtype = 1 if residual.dtype is torch.float32 else 0
+    elif residual_out is not None:
+        raise ValueError("residual_out: given without a residual")
+    if y is not None:
+        py = _fits(y, "y", _BF16, shape, dev)
+    if codes is not None or scales is not None:
+        if codes is None or scales is None:
+            raise ValueError("codes and scales go together")
+        pc = _fits(codes, "codes", _U8, (rows, cols if mma_type == MOE_MMA_FP8_X_MXF4 else cols // 2), dev)
+        ps = _fits(scales, "scales", _U8, (rows, cols // (16 if mma_type == MOE_MMA_NVF4_X_NVF4 else 32)), dev)
+    st = _lib.moe_w4a4_add_rmsnorm(mma_type, res_dtype, 1 if weight.dtype is torch.float32 else 0, rows, cols, px, pr,
+                                   pw, eps, tensor_scale, pro, py, pc, ps, _raw_stream(stream, dev))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_w4a4_add_rmsnorm")
+
+
+def moe_w4a4_router(logits, topk_ids, topk_weights, bias=None, scoring: int = MOE_SCORE_SOFTMAX, num_groups: int = 1,
+                    topk_groups: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """Experts and weights of every token from the router's logits: logits bf16
+    / float32 [T, E]; bias None or float32 [E] (added to the scores for the
+    choice only); topk_ids int32 [T, k] and topk_weights float32 [T, k] are
+    written (k is their width), ready for a forward."""
+    dev = _device_of(logits, "logits")
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError(f"logits {tuple(logits.shape)} and topk_ids {tuple(topk_ids.shape)}: expected [T, E] and [T, k]")
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    pl = _fits(logits, "logits", _BF16_F32, (T, E), dev)
+    pi = _fits(topk_ids, "topk_ids", _I32, (T, k), dev)
+    pw = _fits(topk_weights, "topk_weights", _F32, (T, k), dev)
+    pb = None if bias is None else _fits(bias, "bias", _F32, (E,), dev)
+    st = _lib.moe_w4a4_router(1 if logits.dtype is torch.float32 else 0, scoring, T, E, k, num_groups, topk_groups, pl,
+                              pb, 1 if renormalize else 0, scale, pi, pw, _raw_stream(stream, dev))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_w4a4_router")
+
+
+def make_linear_cfg(in_features: int, out_features: int, max_tokens: int,
+                    mma_type: int = MOE_MMA_MXF4_X_MXF4) -> moe_w4a4_linear_cfg:
+    return moe_w4a4_linear_cfg(in_features, out_features, max_tokens, mma_type)
+
+
+def moe_w4a4_linear_query(cfg: moe_w4a4_linear_cfg):
+    """(prepared_bytes, workspace_bytes)."""
+    p, w = _sz(), _sz()
+    _check(_lib.moe_w4a4_linear_query(ctypes.byref(cfg), ctypes.byref(p), ctypes.byref(w)), "moe_w4a4_linear_query")
+    return p.value, w.value
+
+
+def moe_w4a4_linear_prepare(cfg: moe_w4a4_linear_cfg, codes, scales, prepared, stream=None) -> None:
+    """codes uint8 [N, K/2], scales uint8 [N, K/32]: canonical MXFP4 weights."""
+    dev = _device_of(codes, "codes")
+    N, K = cfg.out_features, cfg.in_features
+    pc = _fits(codes, "codes", _U8, (N, K // 2), dev)
+    ps = _fits(scales, "scales", _U8, (N, K // 32), dev)
+    pw = _fits(prepared, "prepared", _U8, prepared.shape, dev)
+    _check(_lib.moe_w4a4_linear_prepare(ctypes.byref(cfg), pc, ps, pw, prepared.numel(), _raw_stream(stream, dev)),
+           "moe_w4a4_linear_prepare")
+
+
+def moe_w4a4_linear(cfg: moe_w4a4_linear_cfg, prepared, x, out, workspace, xq=None, xsf=None, addend=None,
+                    stream=None) -> None:
+    """out [T, N] (bf16 or float32) = Q(x) W^T (+ addend bf16 [T, N]); x bf16
+    [T, K], or None and xq uint8 [T, K/2] (E4M3: [T, K]) with xsf uint8 [T, K/32]."""
+    dev = _device_of(out, "out")
+    K, N = cfg.in_features, cfg.out_features
+    px = pq = ps = pa = None
+    if x is not None:
+        if xq is not None or xsf is not None:
+            raise ValueError("x: given together with xq or xsf")
+        T = x.shape[0] if x.dim() == 2 else -1
+        px = _fits(x, "x", _BF16, (T, K), dev)
+    else:
+        if xq is None or xsf is None:
+            raise ValueError("either x, or xq and xsf")
+        T = xq.shape[0] if xq.dim() == 2 else -1
+        pq = _fits(xq, "xq", _U8, (T, K if cfg.mma_type == MOE_MMA_FP8_X_MXF4 else K // 2), dev)
+        ps = _fits(xsf, "xsf", _U8, (T, K // 32), dev)
+    if addend is not None:
+        pa = _fits(addend, "addend", _BF16, (T, N), dev)
+    po = _fits(out, "out", _BF16_F32, (T, N), dev)
+    pw = _fits(prepared, "prepared", _U8, prepared.shape, dev)
+    pk = _fits(workspace, "workspace", _U8, workspace.shape, dev)
+    st = _lib.moe_w4a4_linear(ctypes.byref(cfg), pw, T, px, pq, ps, pa, 1 if out.dtype is torch.float32 else 0, po, pk,
+                              workspace.numel(), _raw_stream(stream, dev))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_w4a4_linear")

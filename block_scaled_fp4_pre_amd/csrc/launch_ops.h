@@ -1,0 +1,39 @@
+// Host-side launchers of the operators around the layer (norm, router,
+// linear).  Every launcher only enqueues on `stream`; arguments were validated
+// by the caller.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// norm.hip.  act: codes of 0 MXFP4, 1 MXFP8 E4M3, 2 NVFP4 under g, or -1 none.
+hipError_t launch_add_rmsnorm(int act, bool res_f32, bool w_f32, int64_t rows, int cols, const uint16_t* x,
+                              const void* residual, const void* weight, float eps, float g, void* residual_out,
+                              uint16_t* y, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+// router.hip
+hipError_t launch_router(bool logits_bf16, int scoring, int64_t T, int E, int k, int groups, int keep,
+                         const void* logits, const float* bias, bool renormalize, float scale, int32_t* ids,
+                         float* weights, hipStream_t stream);
+
+// linear_prepare.hip: canonical MXFP4 weights -> tile order, zeros in the padding.
+hipError_t launch_linear_prepare(const uint8_t* codes, const uint8_t* scales, int N, int K, int units, int steps,
+                                 uint8_t* p_codes, uint8_t* p_scales, hipStream_t stream);
+// Tokens -> the same tile order (units of 64 tokens, fp8: two 1 KiB pieces per
+// 16 tokens and step): x quantized, or xq / xsf copied.
+hipError_t launch_linear_tokens(bool fp8, const uint16_t* x, const uint8_t* xq, const uint8_t* xsf, int T, int K,
+                                int units, int steps, uint8_t* t_codes, uint8_t* t_scales, hipStream_t stream);
+
+// The product over tile-ordered operands (linear.hip).
+struct LinearArgs {
+  const uint8_t *wc, *ws;      // weights
+  const uint8_t *tc, *ts;      // tokens
+  const uint16_t* addend;      // or null
+  void* out;
+  int T, N, steps;
+  bool out_f32;
+};
+hipError_t launch_linear(bool fp8, const LinearArgs& a, hipStream_t stream);
+
+}  // namespace moe

@@ -159,4 +159,111 @@ int check_stage_args(const moe_w4a4_cfg* cfg, const void* prepared, int32_t num_
   return MOE_OK;
 }
 
+int check_norm_args(int32_t mma_type, int32_t res_dtype, int32_t w_dtype, int64_t rows, int32_t cols, const void* x,
+                    const void* residual, const void* weight, float eps, float g, const void* residual_out,
+                    const void* y, const void* codes, const void* scales, bool* noop) {
+  *noop = false;
+  if ((res_dtype != 0 && res_dtype != 1) || (w_dtype != 0 && w_dtype != 1)) return MOE_EUNSUPPORTED;
+  if (rows < 0 || cols <= 0 || !(eps > 0.0f && eps <= 3.402823466e38f)) return MOE_EINVAL;
+  if (cols % 32 != 0 || cols > kNormMaxCols || rows >= (int64_t)1 << 31) return MOE_EUNSUPPORTED;
+  if (rows == 0) {
+    *noop = true;
+    return MOE_OK;
+  }
+  if (x == nullptr || weight == nullptr || (y == nullptr && codes == nullptr)) return MOE_EINVAL;
+  if ((residual == nullptr) != (residual_out == nullptr) || (codes == nullptr) != (scales == nullptr)) return MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+      !aligned(y, 16) || !aligned(codes, 16))
+    return MOE_EINVAL;
+  if (codes != nullptr) {
+    if (mma_type != MOE_MMA_MXF4_X_MXF4 && mma_type != MOE_MMA_FP8_X_MXF4 && mma_type != MOE_MMA_NVF4_X_NVF4)
+      return MOE_EUNSUPPORTED;
+    if (mma_type == MOE_MMA_NVF4_X_NVF4 && !nv_scale_ok(g)) return MOE_EINVAL;
+  }
+  return MOE_OK;
+}
+
+int check_router_args(int32_t logits_dtype, int32_t scoring, int64_t num_tokens, int32_t num_experts, int32_t topk,
+                      int32_t num_groups, int32_t topk_groups, const void* logits, const void* bias, float scale,
+                      const void* topk_ids, const void* topk_weights, bool* noop) {
+  *noop = false;
+  if (logits_dtype != 0 && logits_dtype != 1) return MOE_EUNSUPPORTED;
+  if (scoring != MOE_SCORE_SOFTMAX && scoring != MOE_SCORE_SIGMOID && scoring != MOE_SCORE_SQRTSOFTPLUS)
+    return MOE_EUNSUPPORTED;
+  if (num_tokens < 0 || num_experts <= 0 || topk <= 0 || num_groups <= 0 || topk_groups <= 0) return MOE_EINVAL;
+  if (!(scale >= -3.402823466e38f && scale <= 3.402823466e38f)) return MOE_EINVAL;
+  if (num_experts > kMaxExperts || topk > kMaxTopk || num_groups > kRouterMaxGroups) return MOE_EUNSUPPORTED;
+  if (num_experts % num_groups != 0 || topk_groups > num_groups ||
+      topk > topk_groups * (num_experts / num_groups))
+    return MOE_EINVAL;
+  if (num_tokens >= ((int64_t)1 << 40) / num_experts) return MOE_EUNSUPPORTED;
+  if (num_tokens == 0) {
+    *noop = true;
+    return MOE_OK;
+  }
+  if (logits == nullptr || topk_ids == nullptr || topk_weights == nullptr) return MOE_EINVAL;
+  if (!aligned(logits, logits_dtype == 0 ? 2 : 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) ||
+      !aligned(topk_weights, 4))
+    return MOE_EINVAL;
+  return MOE_OK;
+}
+
+int check_linear_cfg(const moe_w4a4_linear_cfg* c) {
+  if (c == nullptr) return MOE_EINVAL;
+  if (c->in_features <= 0 || c->out_features <= 0 || c->max_tokens < 0) return MOE_EINVAL;
+  if (c->in_features % 32 != 0 || c->in_features > kLinearMaxK || c->out_features > kLinearMaxN ||
+      c->max_tokens > kLinearMaxTokens || (int64_t)c->max_tokens * c->out_features > kLinearMaxOut)
+    return MOE_EUNSUPPORTED;
+  if (c->mma_type != MOE_MMA_MXF4_X_MXF4 && c->mma_type != MOE_MMA_FP8_X_MXF4) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+LinearLayout linear_layout(const moe_w4a4_linear_cfg* c) {
+  LinearLayout L{};
+  L.steps = (c->in_features + 127) / 128;
+  L.units = ((uint64_t)c->out_features + 255) / 256 * 4;
+  L.token_units = ((uint64_t)c->max_tokens + 255) / 256 * 4;
+  // per unit and step: 4 KiB of packed E2M1 (E4M3: 8 KiB) and 256 B of scales
+  const uint64_t tok = c->mma_type == MOE_MMA_FP8_X_MXF4 ? 8192 : 4096;
+  L.wc = 0;
+  L.ws = L.units * L.steps * 4096;
+  L.prepared = L.ws + L.units * L.steps * 256;
+  L.tc = 0;
+  L.ts = L.token_units * L.steps * tok;
+  L.workspace = L.ts + L.token_units * L.steps * 256;
+  return L;
+}
+
+int check_linear_prepare_args(const moe_w4a4_linear_cfg* cfg, const void* codes, const void* scales,
+                              const void* prepared, size_t prepared_bytes) {
+  const int st = check_linear_cfg(cfg);
+  if (st != MOE_OK) return st;
+  if (!codes || !scales || !prepared) return MOE_EINVAL;
+  if (!aligned(codes, 16) || !aligned(prepared, 256)) return MOE_EINVAL;
+  if (prepared_bytes < linear_layout(cfg).prepared) return MOE_EWORKSPACE;
+  return MOE_OK;
+}
+
+int check_linear_args(const moe_w4a4_linear_cfg* cfg, const void* prepared, int32_t num_tokens, const void* x,
+                      const void* xq, const void* xsf, const void* addend, int32_t out_dtype, const void* out,
+                      const void* workspace, size_t workspace_bytes, bool* noop) {
+  *noop = false;
+  const int st = check_linear_cfg(cfg);
+  if (st != MOE_OK) return st;
+  if (out_dtype != 0 && out_dtype != 1) return MOE_EUNSUPPORTED;
+  if (num_tokens < 0) return MOE_EINVAL;
+  if (num_tokens > cfg->max_tokens) return MOE_ECAPACITY;
+  if (num_tokens == 0) {
+    *noop = true;
+    return MOE_OK;
+  }
+  if (prepared == nullptr || out == nullptr || workspace == nullptr) return MOE_EINVAL;
+  if (x != nullptr ? xq != nullptr || xsf != nullptr : xq == nullptr || xsf == nullptr) return MOE_EINVAL;
+  if (!aligned(prepared, 256) || !aligned(workspace, 256) || !aligned(x, 16) || !aligned(xq, 16) ||
+      !aligned(addend, 16) || !aligned(out, 16))
+    return MOE_EINVAL;
+  if (workspace_bytes < linear_layout(cfg).workspace) return MOE_EWORKSPACE;
+  return MOE_OK;
+}
+
 }  // namespace moe

@@ -90,4 +90,37 @@ int check_stage_args(const moe_w4a4_cfg* cfg, const void* prepared, int32_t num_
                      const void* topk_ids, const void* topk_weights, const void* out, const void* workspace,
                      size_t workspace_bytes, uint32_t stages, const void* gemm1_acc, bool* noop);
 
+// ---- operators around the layer ----
+constexpr int kNormMaxCols = 65536;
+constexpr int kRouterMaxGroups = 64;      // one lane of a wave each
+constexpr int kLinearMaxK = 65536;
+constexpr int kLinearMaxN = 1 << 20;
+constexpr int kLinearMaxTokens = 1 << 20;
+constexpr int64_t kLinearMaxOut = (int64_t)1 << 34;   // tokens * N: the product's launch stays below 2^32 threads
+
+// Arguments of moe_w4a4_add_rmsnorm and moe_w4a4_router; *noop: no rows.
+int check_norm_args(int32_t mma_type, int32_t res_dtype, int32_t w_dtype, int64_t rows, int32_t cols, const void* x,
+                    const void* residual, const void* weight, float eps, float g, const void* residual_out,
+                    const void* y, const void* codes, const void* scales, bool* noop);
+int check_router_args(int32_t logits_dtype, int32_t scoring, int64_t num_tokens, int32_t num_experts, int32_t topk,
+                      int32_t num_groups, int32_t topk_groups, const void* logits, const void* bias, float scale,
+                      const void* topk_ids, const void* topk_weights, bool* noop);
+
+// A linear's tiles (tiles.h, with 4 units = 256 rows a group): weights and
+// tokens are padded to whole groups of rows and whole K steps of 128.
+struct LinearLayout {
+  uint64_t steps;                 // K steps of 128
+  uint64_t units;                 // 64-row units of W, a multiple of 4
+  uint64_t token_units;           // 64-row units of max_tokens tokens, a multiple of 4
+  uint64_t wc, ws, prepared;      // offsets of codes and scales in the prepared weights, and its size
+  uint64_t tc, ts, workspace;     // the same of the quantized tokens in the workspace
+};
+int check_linear_cfg(const moe_w4a4_linear_cfg* c);
+LinearLayout linear_layout(const moe_w4a4_linear_cfg* c);   // c must pass check_linear_cfg
+int check_linear_prepare_args(const moe_w4a4_linear_cfg* cfg, const void* codes, const void* scales,
+                              const void* prepared, size_t prepared_bytes);
+int check_linear_args(const moe_w4a4_linear_cfg* cfg, const void* prepared, int32_t num_tokens, const void* x,
+                      const void* xq, const void* xsf, const void* addend, int32_t out_dtype, const void* out,
+                      const void* workspace, size_t workspace_bytes, bool* noop);
+
 }  // namespace moe

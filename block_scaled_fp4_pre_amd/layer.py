@@ -151,3 +151,66 @@ class MoeW4A4Layer:
             n *= s
         nbytes = n * torch.empty((), dtype=dtype).element_size()
         return self.workspace[off:off + nbytes].view(dtype).view(*shape)
+
+
+class W4A4Linear:
+    """A dense linear with MXFP4 weights (moe_w4a4_linear): owns the prepared
+    weights and the workspace for max_tokens tokens."""
+
+    def __init__(self, in_features: int, out_features: int, max_tokens: int,
+                 device: str | torch.device = "cuda", mma_type: int = _lib.MOE_MMA_MXF4_X_MXF4,
+                 prepared: torch.Tensor | None = None):
+        """mma_type: MOE_MMA_MXF4_X_MXF4 (tokens quantized to MXFP4) or
+        MOE_MMA_FP8_X_MXF4 (MXFP8 E4M3).  prepared: the weights of another
+        linear of the same shape to share (see with_capacity)."""
+        self.K, self.N, self.max_tokens, self.mma_type = in_features, out_features, max_tokens, mma_type
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.cfg = _lib.make_linear_cfg(in_features, out_features, max_tokens, mma_type)
+        pb, wb = _lib.moe_w4a4_linear_query(self.cfg)
+        if prepared is None:
+            prepared = torch.empty(pb, dtype=torch.uint8, device=self.device)
+        elif prepared.numel() < pb or prepared.device != self.device:
+            raise ValueError("shared prepared buffer is too small or on another device")
+        self.prepared = prepared
+        self.workspace = torch.empty(max(wb, 1), dtype=torch.uint8, device=self.device)
+
+    def with_capacity(self, max_tokens: int, mma_type: int | None = None) -> "W4A4Linear":
+        """A linear over the same prepared weights with its own workspace."""
+        return W4A4Linear(self.K, self.N, max_tokens, self.device,
+                          self.mma_type if mma_type is None else mma_type, prepared=self.prepared)
+
+    def load_canonical(self, codes, scales) -> None:
+        """codes uint8 [N, K/2] and scales uint8 [N, K/32], MXFP4 (moe_w4a4_quantize)."""
+        with torch.cuda.device(self.device):
+            _lib.moe_w4a4_linear_prepare(self.cfg, codes, scales, self.prepared)
+
+    def load_fp32(self, weight) -> None:
+        """weight [N, K] (host or device), quantized to MXFP4 on the device."""
+        w = torch.as_tensor(weight).to(self.device, torch.float32).contiguous()
+        codes = torch.empty((self.N, self.K // 2), dtype=torch.uint8, device=self.device)
+        scales = torch.empty((self.N, self.K // 32), dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(self.device):
+            _lib.moe_w4a4_quantize(w, codes, scales)
+            _lib.moe_w4a4_linear_prepare(self.cfg, codes, scales, self.prepared)
+
+    def _run(self, x, xq, xsf, out, addend, dtype, stream):
+        if out is None:
+            T = (x if x is not None else xq).shape[0]
+            out = torch.empty((T, self.N), dtype=dtype, device=self.device)
+        if torch.cuda.current_device() == self.device.index:
+            _lib.moe_w4a4_linear(self.cfg, self.prepared, x, out, self.workspace, xq, xsf, addend, stream)
+        else:
+            with torch.cuda.device(self.device):
+                _lib.moe_w4a4_linear(self.cfg, self.prepared, x, out, self.workspace, xq, xsf, addend, stream)
+        return out
+
+    def forward(self, x, out=None, addend=None, dtype=torch.bfloat16, stream=None):
+        """x bf16 [T, K] -> out [T, N] (bf16 or float32; made of `dtype` if
+        None); addend bf16 [T, N] is added before the rounding (may be out)."""
+        return self._run(x, None, None, out, addend, dtype, stream)
+
+    def forward_quantized(self, codes, scales, out=None, addend=None, dtype=torch.bfloat16, stream=None):
+        """The same from tokens quantized before (moe_w4a4_add_rmsnorm, moe_w4a4_quantize)."""
+        return self._run(None, codes, scales, out, addend, dtype, stream)

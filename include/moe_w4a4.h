@@ -272,6 +272,125 @@ int moe_w4a4_forward_noalloc(const moe_w4a4_cfg* cfg, const void* prepared, int3
                              const uint16_t* x, const int32_t* topk_ids, const float* topk_weights,
                              uint16_t* out, void* stream);
 
+/* ---- operators around the layer ---------------------------------------- */
+
+/* Residual addition, root-mean-square norm and quantization of `rows` rows of
+ * `cols` values: the producer of the tokens a forward or a linear reads.
+ *   h = x                          without a residual (residual == NULL), else
+ *   h = rnd(x + residual)          one rounding to the residual's own type;
+ *   n = h * weight / sqrt(mean(h^2 along the row) + eps)
+ *   y = n rounded to float32, then to bfloat16;
+ *   codes, scales = y quantized as the activations of mma_type (the rules
+ *                   above; NVFP4 under the tensor scale g): byte for byte what
+ *                   pre-dispatch makes of y.
+ * The squares' sum, the norm and the product with the weight are computed in
+ * fp64: a last bit lost in front of a quantizer moves values next to one of its
+ * borders by a whole step.  Results do not depend on the launch shape in
+ * practice (the fp64 sums differ in their last bits only).
+ *   x            device bfloat16 [rows, cols]
+ *   residual     NULL, or device [rows, cols] of res_dtype (0 = bfloat16, 1 = float32)
+ *   weight       device [cols] of w_dtype (0 = bfloat16, 1 = float32)
+ *   residual_out device [rows, cols] of res_dtype: h; NULL exactly when residual is.
+ *                May be `residual` itself (or x, if that has its type)
+ *   y            NULL, or device bfloat16 [rows, cols]; may be x itself
+ *   codes        NULL, or device uint8 [rows, cols/2] (E4M3: [rows, cols])
+ *   scales       uint8 [rows, cols/32] (NVFP4: cols/16); NULL exactly when codes is
+ * x, residual, weight, residual_out, y and codes 16-byte aligned; no other
+ * overlap of inputs and outputs than the three named.  cols % 32 == 0, cols <=
+ * 65536, rows >= 0 (0 enqueues nothing and looks at no pointer), eps finite
+ * and > 0; without codes mma_type and g are not looked at.  y or codes must be
+ * given.  Values must be finite, and so must x + residual: a row with others
+ * gets a y with NaN or infinity in it and unspecified codes; other rows are
+ * untouched by it.  xq and xsf of the forward's workspace may be the codes and
+ * scales here: moe_w4a4_run_stages without MOE_STAGE_QUANT then starts from
+ * them. */
+int moe_w4a4_add_rmsnorm(int32_t mma_type, int32_t res_dtype, int32_t w_dtype, int64_t rows, int32_t cols,
+                         const uint16_t* x, const void* residual, const void* weight, float eps, float g,
+                         void* residual_out, uint16_t* y, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* scoring: a router logit's score.  SOFTMAX over the row's experts, SIGMOID
+ * 1 / (1 + exp(-l)), SQRTSOFTPLUS sqrt(log(1 + exp(l))). */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1, MOE_SCORE_SQRTSOFTPLUS = 2 };
+
+/* The router's choice: topk_ids and topk_weights of every forward from the
+ * logits of the num_experts experts.  Per token:
+ *   s[e]   = score of logit l[e], computed in fp64 and rounded to float32;
+ *   c[e]   = l[e] when bias is NULL (every scoring rises with the logit), else
+ *            s[e] + bias[e] in float32;
+ *   groups: experts [j*num_experts/num_groups, ...) are group j; its rank is its
+ *            largest c without a bias, the sum of its two largest with one (of
+ *            its only one, if no second is left); the topk_groups groups of
+ *            the highest rank stay (num_groups == 1: all experts stay);
+ *   ids    = the topk experts of the largest c that stay, in falling order,
+ *            equal ones (groups too) by the lower index;
+ *   weights = s[ids], divided by (their sum + 1e-20) when renormalize is not
+ *            0, times scale.
+ * An expert whose logit or c is -infinity or NaN is not chosen (masked or out
+ * of service).  Slots for which no expert is left get id -1 and weight 0: a
+ * forward skips them.  A logit of +infinity counts as the largest float.
+ * A softmax is taken over all experts whose logit is not -infinity or NaN.
+ *   logits        device [num_tokens, num_experts] of logits_dtype (0 =
+ *                 bfloat16, 1 = float32)
+ *   bias          NULL, or device float32 [num_experts]
+ *   topk_ids      device int32 [num_tokens, topk]
+ *   topk_weights  device float32 [num_tokens, topk]
+ * All aligned to their element size.  1 <= num_experts <= 512, 1 <= topk <= 16,
+ * num_groups (at most 64) divides num_experts, 1 <= topk_groups <= num_groups,
+ * topk <= topk_groups * (num_experts / num_groups), scale finite; num_tokens >=
+ * 0 (0 enqueues nothing and looks at no pointer) and num_tokens * num_experts
+ * < 2^40. */
+int moe_w4a4_router(int32_t logits_dtype, int32_t scoring, int64_t num_tokens, int32_t num_experts, int32_t topk,
+                    int32_t num_groups, int32_t topk_groups, const void* logits, const float* bias,
+                    int32_t renormalize, float scale, int32_t* topk_ids, float* topk_weights, void* stream);
+
+/* A dense linear with MXFP4 weights (projections, shared experts, output
+ * heads): out[t, n] = sum over k of Q(x)[t, k] * W[n, k] (+ addend[t, n]).
+ * Q is the activation quantizer of mma_type (MOE_MMA_MXF4_X_MXF4 or
+ * MOE_MMA_FP8_X_MXF4; MOE_MMA_NVF4_X_NVF4 is not built: MOE_EUNSUPPORTED).
+ * Supported: in_features % 32 == 0, 32 <= in_features <= 65536, 1 <=
+ * out_features <= 2^20, 0 <= max_tokens <= 2^20, max_tokens * out_features <=
+ * 2^34. */
+typedef struct moe_w4a4_linear_cfg {
+  int32_t in_features;   /* K */
+  int32_t out_features;  /* N */
+  int32_t max_tokens;    /* capacity of the workspace */
+  int32_t mma_type;
+} moe_w4a4_linear_cfg;
+
+/* Sizes in bytes of the prepared weights and of the workspace of a linear;
+ * either output may be NULL.  Pure host function. */
+int moe_w4a4_linear_query(const moe_w4a4_linear_cfg* cfg, size_t* prepared_bytes, size_t* workspace_bytes);
+
+/* Re-lay canonical MXFP4 weights (codes uint8 [N, K/2], 16-byte aligned;
+ * scales uint8 [N, K/32]; device) into the operand order of the product, once
+ * at load time: a byte permutation, with zeros where N and K are padded to
+ * whole tiles.  prepared: device buffer of query's prepared_bytes, 256-byte
+ * aligned. */
+int moe_w4a4_linear_prepare(const moe_w4a4_linear_cfg* cfg, const uint8_t* codes, const uint8_t* scales,
+                            void* prepared, size_t prepared_bytes, void* stream);
+
+/* The product for num_tokens tokens (0 <= num_tokens <= max_tokens; 0 enqueues
+ * nothing and looks at no pointer).  Either x (device bfloat16 [num_tokens, K],
+ * finite) is given, and quantized on the way in, or xq and xsf (codes uint8
+ * [num_tokens, K/2], E4M3: [num_tokens, K], and scales uint8 [num_tokens,
+ * K/32] as moe_w4a4_quantize, moe_w4a4_add_rmsnorm or a forward's pre-dispatch
+ * make them).  The result is the same, bit for bit.
+ *   addend     NULL, or device bfloat16 [num_tokens, N], added to the fp32 sum
+ *              before the one rounding; may be `out` itself when that is bfloat16
+ *   out_dtype  0 = bfloat16, 1 = float32
+ *   out        device [num_tokens, N] of out_dtype
+ *   workspace  device buffer of query's workspace_bytes, 256-byte aligned: the
+ *              quantized tokens in operand order (not kept from call to call,
+ *              any contents at the start; calls that share one must not overlap)
+ * x, xq, addend and out 16-byte aligned, xsf by bytes.  Sums are fp32 in the
+ * matrix cores, in a fixed order (the result is deterministic; sums of
+ * another num_tokens may be ordered otherwise).  With E4M3 tokens the matrix
+ * cores drop bits of products 2^13 below the largest of eight neighbours.
+ * Errors as for moe_w4a4_forward. */
+int moe_w4a4_linear(const moe_w4a4_linear_cfg* cfg, const void* prepared, int32_t num_tokens, const uint16_t* x,
+                    const uint8_t* xq, const uint8_t* xsf, const uint16_t* addend, int32_t out_dtype, void* out,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* moe_w4a4_status_string(int status);
 

@@ -13,6 +13,9 @@ Plain, slow, fp64 NumPy code that follows the method step by step:
   route    stable counting sort of routed rows by expert
   forward  quantize -> route -> GEMM1 + SwiGLU -> requantize -> GEMM2 -> combine
   dense    brute force: every expert on every token, masked by the routing
+  norm     residual addition and root-mean-square norm
+  router   scores, groups and top-k of the router's logits
+  linear   dense product with MXFP4 weights, and a device's error bound
 
 Pages cited in this package:
   [P1] sglang PR "[deepseek-v4] Bump sgl-deep-gemm for packed FP4xFP4 mega-MoE
@@ -30,4 +33,4 @@ Pins: tests/test_oracle_*.py check every function against closed forms, brute
 force and invariants. Where no pin exists a function's docstring says
 "parity unpinned".
 """
-from . import bf16, dense, forward, mxfp4, mxfp8, nvfp4, route  # noqa: F401
+from . import bf16, dense, forward, linear, mxfp4, mxfp8, norm, nvfp4, route, router  # noqa: F401

@@ -1,0 +1,160 @@
+"""GPU tier: moe_w4a4_linear against the fp64 oracle.
+
+Tolerance: oracle.linear.sum_error (the matrix cores' sums), then half a step
+of the output's type: 2^-8 (bfloat16), 2^-24 (float32) of the value."""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_fp4_pre_amd import _lib
+from block_scaled_fp4_pre_amd.layer import W4A4Linear
+from oracle import bf16, linear, mxfp4
+from tests.gpu_support import dev, dev_bf16, log
+
+pytestmark = pytest.mark.gpu
+
+MX4, FP8 = _lib.MOE_MMA_MXF4_X_MXF4, _lib.MOE_MMA_FP8_X_MXF4
+TYPES = pytest.mark.parametrize("mma", [MX4, FP8], ids=["mxf4xmxf4", "fp8xfp4"])
+
+
+def tokens(T, K, seed):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(size=(T, K)) * np.exp(0.5 * rng.normal(size=K)) * np.exp(0.3 * rng.normal(size=(T, 1)))
+    return bf16.encode(x.astype(np.float32).astype(np.float64))
+
+
+def weights(N, K, seed):
+    return mxfp4.quantize_packed((0.02 * np.random.default_rng(seed).normal(size=(N, K))).astype(np.float32))
+
+
+def make_linear(K, N, max_tokens, mma, wc, ws):
+    lin = W4A4Linear(K, N, max_tokens, mma_type=mma)
+    lin.prepared.fill_(0xA5)                      # the padding is the library's to write
+    lin.workspace.fill_(0xA5)
+    lin.load_canonical(dev(wc), dev(ws))
+    return lin
+
+
+def reference(x, wc, ws, mma, addend=None):
+    c, s = linear.quantize_tokens(bf16.decode(x), mma == FP8)
+    return (c, s) + linear.linear(c, s, wc, ws, mma == FP8, addend)
+
+
+def close(got, ref, mag, K, mma, f32=False):
+    err = np.abs(got - ref)
+    tol = linear.sum_error(mag, K, mma == FP8)
+    tol = tol + (np.abs(ref) + tol) * (2.0 ** -24 if f32 else 2.0 ** -8)
+    assert np.all(np.isfinite(got))
+    assert np.all(err <= tol), (float((err / tol).max()), np.argwhere(err > tol)[:4])
+
+
+def run(lin, x, T, N, dtype=torch.bfloat16, addend=None, quantized=None):
+    """The call on rows [0, T) of a larger buffer whose other rows must stay."""
+    buf = torch.full((T + 2, N), 77.0, dtype=dtype, device="cuda")
+    if quantized is None:
+        lin.forward(dev_bf16(x), out=buf[:T], addend=addend)
+    else:
+        lin.forward_quantized(*(dev(q) for q in quantized), out=buf[:T], addend=addend)
+    torch.cuda.synchronize()
+    assert torch.all(buf[T:] == 77.0)
+    return buf[:T]
+
+
+SIZES = [(1, 32, 1), (1, 64, 16), (1, 4096, 4096), (2, 96, 17), (3, 128, 64), (8, 160, 100), (15, 2048, 65), (16, 2080, 256),
+         (17, 1056, 257), (31, 4096, 130), (32, 512, 1111), (33, 8192, 48), (48, 96, 2048), (63, 1024, 63),
+         (64, 4096, 512), (65, 256, 300), (100, 3200, 1023), (128, 128, 128), (130, 416, 515), (255, 2048, 255),
+         (256, 1024, 1024), (257, 32, 4096), (300, 1056, 1111), (513, 640, 260), (1030, 4096, 520)]
+
+
+@TYPES
+@pytest.mark.parametrize("T,K,N", SIZES)
+def test_sizes(T, K, N, mma):
+    log(f"[test] linear T {T} K {K} N {N} mma {mma}")
+    x, (wc, ws) = tokens(T, K, T + K), weights(N, K, N)
+    lin = make_linear(K, N, T, mma, wc, ws)
+    c, s, ref, mag = reference(x, wc, ws, mma)
+    got = run(lin, x, T, N)
+    close(got.double().cpu().numpy(), ref, mag, K, mma)
+    again = run(lin, x, T, N, quantized=(c, s))
+    assert torch.equal(got, again)                # from tokens quantized before: the same bits
+    f32 = run(lin, x, T, N, dtype=torch.float32)
+    close(f32.double().cpu().numpy(), ref, mag, K, mma, f32=True)
+    assert torch.equal(f32.to(torch.bfloat16), got)
+
+
+@TYPES
+@pytest.mark.parametrize("T,K,N", [(1, 512, 100), (16, 2048, 512), (40, 96, 77), (300, 1056, 260), (600, 512, 1024)])
+def test_addend_apart_and_in_place(T, K, N, mma):
+    log(f"[test] linear addend T {T} K {K} N {N} mma {mma}")
+    x, (wc, ws) = tokens(T, K, 5), weights(N, K, 6)
+    add = tokens(T, N, 7)
+    lin = make_linear(K, N, T + 9, mma, wc, ws)   # a workspace for more tokens than the call's
+    _, _, ref, mag = reference(x, wc, ws, mma, bf16.decode(add))
+    got = run(lin, x, T, N, addend=dev_bf16(add))
+    close(got.double().cpu().numpy(), ref, mag + np.abs(bf16.decode(add)), K, mma)
+    out = dev_bf16(add)
+    lin.forward(dev_bf16(x), out=out, addend=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, got)
+    f32 = run(lin, x, T, N, dtype=torch.float32, addend=dev_bf16(add))
+    assert torch.equal(f32.to(torch.bfloat16), got)
+
+
+@TYPES
+def test_scales_at_their_ends(mma):
+    """Tokens of zeros, subnormals, and rows 2^+-60 apart; weights with scale
+    bytes 0 and near the largest: exact powers of two throughout."""
+    log(f"[test] linear extreme scales mma {mma}")
+    T, K, N = 20, 256, 48
+    x = tokens(T, K, 8)
+    v = bf16.decode(x)
+    v[0] = 0
+    v[1] *= 2.0 ** 60
+    v[2] *= 2.0 ** -60
+    v[3, 32:] = 0
+    v[4, :32] = 0
+    v[5] = 2.0 ** -130
+    x = bf16.encode(v)
+    wc, ws = weights(N, K, 9)
+    ws[0], wc[0] = 0, 0                           # a row of zeros as the quantizer writes it
+    ws[1] = 127 + 40
+    ws[2] = 127 - 60
+    lin = make_linear(K, N, T, mma, wc, ws)
+    _, _, ref, mag = reference(x, wc, ws, mma)
+    got = run(lin, x, T, N, dtype=torch.float32).double().cpu().numpy()
+    tol = linear.sum_error(mag, K, mma == FP8)
+    assert np.all(np.abs(got - ref) <= tol + (np.abs(ref) + tol) * 2.0 ** -24 + 2.0 ** -149)
+    assert np.all(got[0] == 0) and np.all(got[:, 0] == 0)
+
+
+@TYPES
+def test_one_set_of_weights_at_several_capacities(mma):
+    log(f"[test] linear with_capacity mma {mma}")
+    K, N = 1024, 640
+    wc, ws = weights(N, K, 10)
+    base = W4A4Linear(K, N, 1, mma_type=MX4)
+    w = mxfp4.dequantize(wc, ws).astype(np.float32)
+    base.load_fp32(w)                             # on the format's grid: quantizes to the same values
+    x = tokens(200, K, 11)
+    big = base.with_capacity(200, mma_type=mma)
+    small = base.with_capacity(7, mma_type=mma)
+    _, _, ref, mag = reference(x, wc, ws, mma)
+    a = run(big, x, 200, N).double().cpu().numpy()
+    close(a, ref, mag, K, mma)
+    b = run(small, x[:7], 7, N).double().cpu().numpy()
+    close(b, ref[:7], mag[:7], K, mma)
+    with pytest.raises(_lib.MoeError) as ei:
+        small.forward(dev_bf16(x[:8]))
+    assert ei.value.status == _lib.MOE_ECAPACITY
+    assert small.forward(torch.empty((0, K), dtype=torch.bfloat16, device="cuda")).shape == (0, N)
+
+
+@TYPES
+def test_repeats_give_the_same_bits(mma):
+    log(f"[test] linear determinism mma {mma}")
+    for T, K, N in ((1, 4096, 4096), (16, 4096, 1024), (64, 8192, 512), (777, 1024, 1536)):
+        x, (wc, ws) = tokens(T, K, 12), weights(N, K, 13)
+        lin = make_linear(K, N, T, mma, wc, ws)
+        first = lin.forward(dev_bf16(x))
+        for _ in range(5):
+            assert torch.equal(lin.forward(dev_bf16(x)), first)
