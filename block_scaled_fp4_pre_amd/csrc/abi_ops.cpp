@@ -80,14 +80,15 @@ int moe_w4a4_linear(const moe_w4a4_linear_cfg* cfg, const void* prepared, int32_
   const uint8_t* pw = static_cast<const uint8_t*>(prepared);
   uint8_t* wsp = static_cast<uint8_t*>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  // tokens in tile order, zeros up to a whole 64-token unit
-  const int units = (num_tokens + 63) / 64;
-  st = hip_status(moe::launch_linear_tokens(fp8, x, xq, xsf, num_tokens, cfg->in_features, units, (int)L.steps,
-                                            wsp + L.tc, wsp + L.ts, s));
-  if (st != MOE_OK) return st;
   const moe::LinearArgs a = {pw + L.wc, pw + L.ws, wsp + L.tc, wsp + L.ts, addend, out, num_tokens, cfg->out_features,
                              (int)L.steps, out_dtype == 1};
-  return hip_status(moe::launch_linear(fp8, a, s));
+  const moe::LinearPlan plan = moe::linear_plan(num_tokens, cfg->out_features);
+  st = hip_status(moe::launch_linear_tokens(fp8, x, xq, xsf, num_tokens, cfg->in_features,
+                                            moe::linear_token_units(plan, num_tokens), (int)L.steps, wsp + L.tc,
+                                            wsp + L.ts, s));
+  if (st != MOE_OK) return st;
+  return hip_status(plan == moe::kLinearSplit ? moe::launch_linear_split(fp8, a, s)
+                                              : moe::launch_linear_tile(fp8, plan, a, s));
 }
 
 }  // extern "C"

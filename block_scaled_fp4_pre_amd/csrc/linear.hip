@@ -6,7 +6,6 @@
 // tokens; its waves split the K steps (wave w takes w, w + 8, ...), each with
 // the whole tile in its accumulators, and their sums meet in LDS, added in wave
 // order.
-#include "gemm_common.h"
 #include "linear_common.h"
 
 namespace moe {
@@ -16,16 +15,16 @@ constexpr int kSplitWaves = 8;
 
 template <bool F8, int NT, int NR>
 struct SplitStep {
-  uint4 a[NR], b[NT], b2[F8 ? NT : 1];
+  v4u a[NR], b[NT], b2[F8 ? NT : 1];
   uint32_t sa, sb;
 };
 
 template <int NR, int NT, bool F8, int R, int C>
 __device__ __forceinline__ void split_mfma(const SplitStep<F8, NT, NR>& s, v4f (&acc)[NT][NR]) {
   if constexpr (F8)
-    acc[C][R] = mfma_fp4_fp8<R, C>(s.a[R], s.b[C], s.b2[C], acc[C][R], (int)s.sa, (int)s.sb);
+    acc[C][R] = mfma_op8<R, C>(s.a[R], s.b[C], s.b2[C], acc[C][R], (int)s.sa, (int)s.sb);
   else
-    acc[C][R] = mfma_fp4<R, C>(s.a[R], s.b[C], acc[C][R], (int)s.sa, (int)s.sb);
+    acc[C][R] = mfma_op<R, C>(s.a[R], s.b[C], acc[C][R], (int)s.sa, (int)s.sb);
   if constexpr (R + 1 < NR)
     split_mfma<NR, NT, F8, R + 1, C>(s, acc);
   else if constexpr (C + 1 < NT)
@@ -60,11 +59,11 @@ __global__ void __launch_bounds__(64 * kSplitWaves) linear_split_kernel(LinearAr
   auto load = [&](int s, SplitStep<F8, NT, NR>& d) {
 #pragma unroll
     for (int r = 0; r < NR; ++r)
-      d.a[r] = *reinterpret_cast<const uint4*>(wc + (size_t)s * (4 * kStepCodeBytes) + r * 1024);
+      d.a[r] = *reinterpret_cast<const v4u*>(wc + (size_t)s * (4 * kStepCodeBytes) + r * 1024);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
-      d.b[c] = *reinterpret_cast<const uint4*>(tc + (size_t)s * (4 * TB) + c * (TB / 4));
-      if constexpr (F8) d.b2[c] = *reinterpret_cast<const uint4*>(tc + (size_t)s * (4 * TB) + c * (TB / 4) + 1024);
+      d.b[c] = *reinterpret_cast<const v4u*>(tc + (size_t)s * (4 * TB) + c * (TB / 4));
+      if constexpr (F8) d.b2[c] = *reinterpret_cast<const v4u*>(tc + (size_t)s * (4 * TB) + c * (TB / 4) + 1024);
     }
     d.sa = *reinterpret_cast<const uint32_t*>(ws + (size_t)s * (4 * kStepScaleBytes)) >> (8 * wb);
     d.sb = *reinterpret_cast<const uint32_t*>(ts + (size_t)s * (4 * kStepScaleBytes)) >> (8 * tb);
@@ -123,7 +122,7 @@ hipError_t launch_linear_type(const LinearArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_linear(bool fp8, const LinearArgs& a, hipStream_t stream) {
+hipError_t launch_linear_split(bool fp8, const LinearArgs& a, hipStream_t stream) {
   return fp8 ? launch_linear_type<true>(a, stream) : launch_linear_type<false>(a, stream);
 }
 

@@ -1,16 +1,39 @@
 // Pieces shared by the kernels of the dense linear.
 #pragma once
-#include "device_common.h"
+#include "gemm_common.h"
 #include "launch_ops.h"
 #include "tiles.h"
 
 namespace moe {
+
+// The block-scaled MFMAs of device_common.h on native vectors: operands that
+// live in arrays across a pipelined loop stay in registers only as these.
+template <int OA, int OB>
+__device__ __forceinline__ v4f mfma_op(const v4u& a, const v4u& b, const v4f& c, int sa, int sb) {
+  const v8i av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const v8i bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, OA, sa, OB, sb);
+}
+template <int OA, int OB>
+__device__ __forceinline__ v4f mfma_op8(const v4u& a, const v4u& lo, const v4u& hi, const v4f& c, int sa, int sb) {
+  const v8i av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const v8i bv = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 0, OA, sa, OB, sb);
+}
 
 // Codes of unit u at K step 0 and the stride to the next step, for operands
 // of CB bytes per unit and step (weights and E2M1 tokens 4096, E4M3 8192).
 template <int CB>
 __device__ __forceinline__ size_t unit_base(int u, int steps) {
   return ((size_t)(u / kGroupUnits) * steps * kGroupUnits + u % kGroupUnits) * CB;
+}
+
+// Two float32 values rounded to bfloat16 (nearest, ties to even; a NaN stays
+// one), `lo` in the low half: v_cvt_pk_bf16_f32.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2bf));
 }
 
 // out[t, n..n+3] = v (+ addend), n a multiple of 4; `whole`: N % 4 == 0, so

@@ -1,0 +1,277 @@
+// The dense linear's product for many tokens: both operands go through LDS.
+//
+// A workgroup of 4 waves (2 x 2) owns 2*WA*16 weight rows x 2*WB*16 tokens, each
+// wave a quarter of it: WA x WB MFMA tiles in its accumulators.  Operands are in
+// tile order, so a K step of the tile is a contiguous run of 1 KiB pieces, copied
+// to LDS as they are by direct-to-LDS loads into a ring of P stages; an operand
+// read is lane l's 16 bytes at 16*l, free of bank conflicts.
+//
+// One barrier a step: a wave passes it when its own DMAs of stage s have landed
+// (in-order vmcnt) and its reads of stage s - 1 are done, so after it stage s may
+// be read and the buffer of stage s - 1 refilled.  The DMAs are inline assembly:
+// the compiler cannot tell the ring's stages apart and would wait for all of them
+// before every LDS read.  Reads and DMAs are issued between the step's MFMAs, and
+// two workgroups share a CU, so that one's MFMAs cover the other's waits.
+#include "linear_common.h"
+
+namespace moe {
+namespace {
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// The 16 (4) bytes at base + voff of lane l go to LDS byte address lds + 16*l
+// (4*l); base and lds are the wave's own (scalar).  M0 carries the LDS address; a DMA right after a scalar write of M0 needs one wait
+// state, which the compiler cannot insert inside an asm statement.
+__device__ __forceinline__ void dma16(const uint8_t* base, int voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const uint8_t* base, int voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+constexpr int kTileWaves = 4;
+
+template <bool F8, int WA, int WB>
+struct TileShape {
+  static constexpr int WAVES = kTileWaves;
+  static constexpr int TB = F8 ? 2048 : 1024;                // token code bytes of a 16-token block and step
+  static constexpr int AB = 2 * WA, BB = 2 * WB;             // 16-row blocks of the tile's two sides
+  static constexpr int A_CODES = 0, B_CODES = AB * 1024;
+  static constexpr int A_SCALES = B_CODES + BB * TB, B_SCALES = A_SCALES + AB / 4 * kStepScaleBytes;
+  static constexpr int BYTES = B_SCALES + BB / 4 * kStepScaleBytes;
+  static constexpr int AD = AB / WAVES, BD = BB * (TB / 1024) / WAVES;   // code DMAs per wave and stage
+  static constexpr int SD = (AB / 4 + BB / 4 + WAVES - 1) / WAVES;       // scale DMAs
+  static constexpr int DMAS = AD + BD + SD;
+  static constexpr int ROWS = AB * 16, TOKENS = BB * 16;
+  static_assert(AD * WAVES == AB && BD * WAVES == BB * (TB / 1024) && AB % 4 == 0 && BB % 4 == 0, "DMA shares");
+};
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(Int<I>{});
+    unrolled<N, I + 1>(f);
+  }
+}
+
+// The wave's outputs acc[token block][row block] to rows t0.. and columns n0..
+// of `out`, G token blocks at a time through `mine` (G*16 x STRIDE bytes of
+// LDS), so that every store covers a whole run of a row: 4*WA lanes a token, 4
+// values a lane.  The loads of a pass's addends are all issued before its
+// first use.  The store loop stays rolled: unrolled over the tokens its code took
+// longer to fetch than to run.
+template <int WA, int WB, int G>
+__device__ __forceinline__ void tile_epilogue(const LinearArgs& p, const v4f (&acc)[WB][WA], uint8_t* mine, int n0,
+                                              int t0, int lane) {
+  constexpr int STRIDE = WA * 16 * 4 + 16;
+  constexpr int LPT = WA * 4, TPP = kWave / LPT, IT = 8;   // lanes a token, tokens a pass, passes in flight
+  const int n = n0 + lane % LPT * 4, tl = lane / LPT;
+  const int left = max(0, min(4, p.N - n));
+  const bool whole = p.N % 4 == 0;                         // then 4 or none are left, and aligned
+  unrolled<WB / G>([&](auto qi) {
+    constexpr int q = decltype(qi)::value;
+#pragma unroll
+    for (int c = 0; c < G; ++c)
+#pragma unroll
+      for (int r = 0; r < WA; ++r)
+        *reinterpret_cast<v4f*>(mine + (c * 16 + (lane & 15)) * STRIDE + (r * 16 + (lane >> 4) * 4) * 4) =
+            acc[q * G + c][r];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int live = left > 0 ? p.T - t0 - q * G * 16 : 0;  // tokens of this part that the lane stores
+#pragma unroll 1
+    for (int i0 = tl; i0 < G * 16; i0 += IT * TPP) {
+      const size_t at = (size_t)(t0 + q * G * 16 + i0) * p.N + n;
+      uint2 add[IT];
+      if (p.addend != nullptr) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          add[i] = make_uint2(0, 0);
+          if (i0 + i * TPP < live) {
+            const uint16_t* a = p.addend + at + (size_t)(i * TPP) * p.N;
+            if (whole) {
+              add[i] = *reinterpret_cast<const uint2*>(a);
+            } else {
+              add[i].x = a[0];
+              if (left > 1) add[i].x |= (uint32_t)a[1] << 16;
+              if (left > 2) add[i].y = a[2];
+              if (left > 3) add[i].y |= (uint32_t)a[3] << 16;
+            }
+          }
+        }
+      }
+      v4f v[IT];
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+        v[i] = *reinterpret_cast<const v4f*>(mine + (i0 + i * TPP) * STRIDE + lane % LPT * 16);
+      if (p.addend != nullptr) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          v[i][0] += bf16_to_f32(add[i].x & 0xFFFFu);
+          v[i][1] += bf16_to_f32(add[i].x >> 16);
+          v[i][2] += bf16_to_f32(add[i].y & 0xFFFFu);
+          v[i][3] += bf16_to_f32(add[i].y >> 16);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        if (i0 + i * TPP >= live) continue;
+        if (p.out_f32) {
+          float* o = static_cast<float*>(p.out) + at + (size_t)(i * TPP) * p.N;
+          if (whole) {
+            *reinterpret_cast<v4f*>(o) = v[i];
+          } else {
+            o[0] = v[i][0];
+            if (left > 1) o[1] = v[i][1];
+            if (left > 2) o[2] = v[i][2];
+            if (left > 3) o[3] = v[i][3];
+          }
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(p.out) + at + (size_t)(i * TPP) * p.N;
+          const uint2 h = make_uint2(pack_bf16(v[i][0], v[i][1]), pack_bf16(v[i][2], v[i][3]));
+          if (whole) {
+            *reinterpret_cast<uint2*>(o) = h;
+          } else {
+            o[0] = (uint16_t)h.x;
+            if (left > 1) o[1] = (uint16_t)(h.x >> 16);
+            if (left > 2) o[2] = (uint16_t)h.y;
+            if (left > 3) o[3] = (uint16_t)(h.y >> 16);
+          }
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  });
+}
+
+template <bool F8, int WA, int WB, int P>
+__global__ void __launch_bounds__(64 * kTileWaves, 2) linear_tile_kernel(LinearArgs p, int row_tiles, int tok_tiles) {
+  using S = TileShape<F8, WA, WB>;
+  constexpr int TB = S::TB;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const uint32_t lbase = (uint32_t)(uintptr_t)lds;
+  // Workgroups are dealt round-robin to the 8 XCDs; each XCD gets a run of the
+  // order below (4 row tiles wide, tokens next), so that the tiles it works on
+  // at a time share their operands in its L2.
+  const int L = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  if (L >= row_tiles * tok_tiles) return;
+  const int band = L / (4 * tok_tiles), width = min(4, row_tiles - band * 4);
+  const int in = L - band * 4 * tok_tiles, tt = in / width, rt = band * 4 + in - tt * width;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wr = wave & 1, wt = wave >> 1;              // the wave's half of the rows, of the tokens
+  const int S_ = p.steps;
+
+  const int au = rt * (S::AB / 4), bu = tt * (S::BB / 4);   // first units of the tile
+  const uint8_t* ac = p.wc + unit_base<kStepCodeBytes>(au, S_) + wave * S::AD * 1024;
+  const uint8_t* bc = p.tc + unit_base<4 * TB>(bu, S_) + wave * S::BD * 1024;
+  // scale units of A, then of B, dealt to the waves in turn (a wave past the
+  // end copies unit 0 of A again: every wave then has as many DMAs in flight)
+  const uint8_t* sc[S::SD];
+  int sdst[S::SD];
+#pragma unroll
+  for (int i = 0; i < S::SD; ++i) {
+    const int u = wave + i * S::WAVES < S::AB / 4 + S::BB / 4 ? wave + i * S::WAVES : 0;
+    sc[i] = u < S::AB / 4 ? p.ws + unit_base<kStepScaleBytes>(au, S_) + u * kStepScaleBytes
+                          : p.ts + unit_base<kStepScaleBytes>(bu, S_) + (u - S::AB / 4) * kStepScaleBytes;
+    sdst[i] = S::A_SCALES + u * kStepScaleBytes;
+  }
+
+  // DMA i of step s's operands into buffer `buf`.
+  auto dma = [&](int s, int buf, int i) {
+    const uint32_t b = lbase + (uint32_t)buf * S::BYTES;
+    if (i < S::AD)
+      dma16(ac + (size_t)s * (4 * kStepCodeBytes) + i * 1024, lane * 16, b + S::A_CODES + (wave * S::AD + i) * 1024);
+    else if (i < S::AD + S::BD)
+      dma16(bc + (size_t)s * (16 * TB) + (i - S::AD) * 1024, lane * 16,
+            b + S::B_CODES + (wave * S::BD + i - S::AD) * 1024);
+    else
+      dma4(sc[i - S::AD - S::BD] + (size_t)s * (4 * kStepScaleBytes), lane * 4, b + sdst[i - S::AD - S::BD]);
+  };
+  // Past the last step the DMAs copy the last stage again (out of L2) into a
+  // buffer that is not read any more, so that every step has as many in flight.
+  auto source = [&](int s) { return min(s, S_ - 1); };
+#pragma unroll 1
+  for (int s = 0; s < P - 1; ++s)
+    for (int i = 0; i < S::DMAS; ++i) dma(source(s), s, i);
+
+  v4f acc[WB][WA];
+#pragma unroll
+  for (int c = 0; c < WB; ++c)
+#pragma unroll
+    for (int r = 0; r < WA; ++r) acc[c][r] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int s = 0, buf = 0; s < S_; ++s) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::DMAS * (P - 2)) : "memory");
+    const uint8_t* st = lds + buf * S::BYTES;
+    const int src = source(s + P - 1), dst = buf == 0 ? P - 1 : buf - 1;
+    v4u a[WA], b[WB], b2[F8 ? WB : 1];
+    int sa[WA / 4], sb[WB / 4];
+#pragma unroll
+    for (int u = 0; u < WA / 4; ++u)
+      sa[u] = *reinterpret_cast<const int*>(st + S::A_SCALES + (wr * (WA / 4) + u) * kStepScaleBytes + lane * 4);
+#pragma unroll
+    for (int u = 0; u < WB / 4; ++u)
+      sb[u] = *reinterpret_cast<const int*>(st + S::B_SCALES + (wt * (WB / 4) + u) * kStepScaleBytes + lane * 4);
+    auto read_b = [&](int c) {
+      const uint8_t* q = st + S::B_CODES + (wt * WB + c) * TB + lane * 16;
+      b[c] = *reinterpret_cast<const v4u*>(q);
+      if constexpr (F8) b2[c] = *reinterpret_cast<const v4u*>(q + 1024);
+    };
+    read_b(0);
+#pragma unroll
+    for (int r = 0; r < WA; ++r)
+      a[r] = *reinterpret_cast<const v4u*>(st + S::A_CODES + (wr * WA + r) * 1024 + lane * 16);
+    unrolled<WA * WB>([&](auto mi) {
+      constexpr int m = decltype(mi)::value, c = m / WA, r = m % WA;
+      if constexpr (r == 0 && c + 1 < WB) read_b(c + 1);
+      if constexpr (F8)
+        acc[c][r] = mfma_op8<r % 4, c % 4>(a[r], b[c], b2[c], acc[c][r], sa[r / 4], sb[c / 4]);
+      else
+        acc[c][r] = mfma_op<r % 4, c % 4>(a[r], b[c], acc[c][r], sa[r / 4], sb[c / 4]);
+      unrolled<S::DMAS>([&](auto di) {
+        constexpr int i = decltype(di)::value;
+        if constexpr (i * (WA * WB) / S::DMAS == m) dma(src, dst, i);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    buf = buf + 1 == P ? 0 : buf + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+
+  constexpr int STRIDE = WA * 16 * 4 + 16, G = S::WAVES * 64 * STRIDE <= P * S::BYTES ? 4 : 2;
+  static_assert(S::WAVES * G * 16 * STRIDE <= P * S::BYTES, "epilogue staging");
+  __syncthreads();                          // every wave is done with the ring
+  tile_epilogue<WA, WB, G>(p, acc, lds + wave * G * 16 * STRIDE, rt * S::ROWS + wr * WA * 16,
+                           tt * S::TOKENS + wt * WB * 16, lane);
+}
+
+template <bool F8, int WA, int WB, int P>
+hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
+  using S = TileShape<F8, WA, WB>;
+  const int64_t rt = (a.N + S::ROWS - 1) / S::ROWS, tt = (a.T + S::TOKENS - 1) / S::TOKENS;
+  auto kern = linear_tile_kernel<F8, WA, WB, P>;
+  const size_t lds = (size_t)P * S::BYTES;
+  static_assert(2 * P * S::BYTES <= 160 * 1024, "two workgroups a CU");
+  const hipError_t err = raise_lds_limit(reinterpret_cast<const void*>(kern), lds);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(kern, dim3((unsigned)((rt * tt + 7) / 8 * 8)), dim3(64 * S::WAVES), lds, stream, a, (int)rt,
+                     (int)tt);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// E4M3 tokens double a stage's token bytes: two stages, still two workgroups a CU.
+hipError_t launch_linear_tile(bool fp8, LinearPlan plan, const LinearArgs& a, hipStream_t stream) {
+  if (plan == kLinearTile256)
+    return fp8 ? launch_tile<true, 8, 4, 2>(a, stream) : launch_tile<false, 8, 4, 3>(a, stream);
+  return fp8 ? launch_tile<true, 4, 4, 3>(a, stream) : launch_tile<false, 4, 4, 4>(a, stream);
+}
+
+}  // namespace moe
