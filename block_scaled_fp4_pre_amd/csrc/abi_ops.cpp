@@ -82,7 +82,9 @@ int moe_w4a4_linear(const moe_w4a4_linear_cfg* cfg, const void* prepared, int32_
   hipStream_t s = static_cast<hipStream_t>(stream);
   const moe::LinearArgs a = {pw + L.wc, pw + L.ws, wsp + L.tc, wsp + L.ts, addend, out, num_tokens, cfg->out_features,
                              (int)L.steps, out_dtype == 1};
-  const moe::LinearPlan plan = moe::linear_plan(num_tokens, cfg->out_features);
+  const moe::LinearPlan plan = moe::linear_plan(num_tokens, cfg->out_features, (int)L.steps);
+  if (plan == moe::kLinearDecode)
+    return hip_status(moe::launch_linear_decode(fp8, a, {x, xq, xsf, num_tokens, cfg->in_features}, s));
   st = hip_status(moe::launch_linear_tokens(fp8, x, xq, xsf, num_tokens, cfg->in_features,
                                             moe::linear_token_units(plan, num_tokens), (int)L.steps, wsp + L.tc,
                                             wsp + L.ts, s));

@@ -34,6 +34,13 @@ struct LinearArgs {
   int T, N, steps;
   bool out_f32;
 };
+// The tokens as the caller gives them: x, or xq and xsf.
+struct LinearInput {
+  const uint16_t* x;
+  const uint8_t *xq, *xsf;
+  int T, K;
+};
+
 // Which kernel takes a product, from its number of 128 x 128 tiles.  Below 128
 // (half the CUs) the split kernel, whose tiles are smaller and whose waves share
 // the K steps; from 128 on the tile kernel, with tiles of 256 rows x 128 tokens
@@ -41,8 +48,12 @@ struct LinearArgs {
 // (split / 128 / 256 rows), MXFP4: 256 x 4096 outputs 8.8 / 13.6 / 21 us, 512 x 4096
 // 15.0 / 14.2 / 22, 64 x 32000 18.6 / 15.8 / 22, 2048 x 4096 58 / 23.9 / 25.1, 4096 x 4096
 // 119 / 41 / 38; E4M3: 512 x 4096 19.1 / 17.6 / 32, 4096 x 4096 - / 55.7 / 54.7.
-enum LinearPlan { kLinearSplit, kLinearTile128, kLinearTile256 };
-inline LinearPlan linear_plan(int T, int N) {
+// Up to kDecodeMaxTokens tokens and kDecodeMaxSteps K steps: the decode kernel,
+// which needs no tokens in tile order.
+constexpr int kDecodeMaxTokens = 16, kDecodeMaxSteps = 64;
+enum LinearPlan { kLinearDecode, kLinearSplit, kLinearTile128, kLinearTile256 };
+inline LinearPlan linear_plan(int T, int N, int steps) {
+  if (T <= kDecodeMaxTokens && steps <= kDecodeMaxSteps) return kLinearDecode;
   const int64_t tt = (T + 127) / 128;
   if (tt * ((N + 127) / 128) < 128) return kLinearSplit;
   return tt * ((N + 255) / 256) >= 512 ? kLinearTile256 : kLinearTile128;
@@ -51,6 +62,7 @@ inline LinearPlan linear_plan(int T, int N) {
 inline int linear_token_units(LinearPlan plan, int T) {
   return plan == kLinearSplit ? (T + 63) / 64 : (T + 127) / 128 * 2;
 }
+hipError_t launch_linear_decode(bool fp8, const LinearArgs& a, const LinearInput& in, hipStream_t stream);   // linear_decode.hip
 hipError_t launch_linear_split(bool fp8, const LinearArgs& a, hipStream_t stream);              // linear.hip
 hipError_t launch_linear_tile(bool fp8, LinearPlan plan, const LinearArgs& a, hipStream_t stream);   // linear_tile.hip
 

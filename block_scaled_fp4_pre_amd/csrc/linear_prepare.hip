@@ -13,7 +13,7 @@
 //
 // Both are bound by HBM: one read of the source, one write of the tiles.
 #include "launch_ops.h"
-#include "quant_group.h"
+#include "quant_e4m3.h"
 #include "tiles.h"
 
 namespace moe {
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) linear_tokens_kernel(const uint16_t* __re
     if constexpr (SRC_BF16) {
       uint32_t w[16];
       load_bf16_words(x, (int64_t)i, w);
-      sc = F8 ? mx8_encode_bf16_group(w, lo, hi) : mx_encode_bf16_group(w, lo);
+      sc = F8 ? mx8_cvt_bf16_group(w, lo, hi) : mx_encode_bf16_group(w, lo);
     } else {
       lo = reinterpret_cast<const uint4*>(xq)[F8 ? 2 * i : i];
       if constexpr (F8) hi = reinterpret_cast<const uint4*>(xq)[2 * i + 1];

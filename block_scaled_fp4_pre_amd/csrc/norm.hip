@@ -15,7 +15,7 @@
 // the same way whatever the order of the sum, so the codes are reproducible
 // next to the quantizer's borders.
 #include "launch_ops.h"
-#include "quant_group.h"
+#include "quant_e4m3.h"
 
 namespace moe {
 namespace {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) add_rmsnorm_kernel(
       if (act == 1) {
         const int e = mx8_scale_exp(amax << 16);
         const float inv = e4m3_exp2(-e);
-        const uint2 q = make_uint2(e4m3_pack4(n[0], n[1], n[2], n[3], inv), e4m3_pack4(n[4], n[5], n[6], n[7], inv));
+        const uint2 q = make_uint2(e4m3_cvt4(n[0], n[1], n[2], n[3], inv), e4m3_cvt4(n[4], n[5], n[6], n[7], inv));
         if (c < pieces) {
           reinterpret_cast<uint2*>(codes)[piece] = q;
           if (c % 4 == 0) scales[piece / 4] = (uint8_t)(e + 127);
