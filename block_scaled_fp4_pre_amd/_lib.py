@@ -327,6 +327,8 @@ def _raw_stream(stream, device_index: int) -> int:
 def _fits(t, name: str, dtypes, shape, device_index: int) -> int:
     """Device address of a contiguous tensor of one of the dtypes, of that
     shape, on device `device_index`; else ValueError."""
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == device_index and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if t.shape != shape:
@@ -349,7 +351,7 @@ def _device_of(t, name: str) -> int:
     """Index of the current device, on which t has to be."""
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a device tensor, got one on {t.device}")
-    return torch.cuda.current_device()
+    return torch._C._cuda_getDevice()      # (t exists, so the runtime is initialised)
 
 
 def moe_w4a4_add_rmsnorm(x, residual, weight, eps: float, residual_out=None, y=None, codes=None, scales=None,

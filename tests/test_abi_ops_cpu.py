@@ -65,7 +65,7 @@ def _t(shape, dtype=torch.bfloat16):
 
 @pytest.fixture
 def current_device_0(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(_lib, "_raw_stream", lambda stream, dev: None)
     monkeypatch.setattr(_lib, "_lib", None)                 # the library must not be reached
 
@@ -112,6 +112,6 @@ def test_linear_binding_refuses(current_device_0, change):
 
 
 def test_binding_refuses_another_device(current_device_0, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     with pytest.raises(ValueError, match="current device"):
         _lib.moe_w4a4_router(_t((4, 64), F32), _t((4, 6), I32), _t((4, 6), F32))
