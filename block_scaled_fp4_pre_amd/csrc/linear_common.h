@@ -2,6 +2,7 @@
 #pragma once
 #include "gemm_common.h"
 #include "launch_ops.h"
+#include "pack_bf16.h"
 #include "tiles.h"
 
 namespace moe {
@@ -26,14 +27,6 @@ __device__ __forceinline__ v4f mfma_op8(const v4u& a, const v4u& lo, const v4u& 
 template <int CB>
 __device__ __forceinline__ size_t unit_base(int u, int steps) {
   return ((size_t)(u / kGroupUnits) * steps * kGroupUnits + u % kGroupUnits) * CB;
-}
-
-// Two float32 values rounded to bfloat16 (nearest, ties to even; a NaN stays
-// one), `lo` in the low half: v_cvt_pk_bf16_f32.
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-  typedef float v2f __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2bf));
 }
 
 // out[t, n..n+3] = v (+ addend), n a multiple of 4; `whole`: N % 4 == 0, so
@@ -66,12 +59,11 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int t, int n, v4f v,
   } else {
     uint16_t* o = static_cast<uint16_t*>(a.out) + i;
     if (whole) {
-      *reinterpret_cast<uint2*>(o) = make_uint2(f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16),
-                                                f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16));
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (j < left) o[j] = (uint16_t)f32_to_bf16(v[j]);
+        if (j < left) o[j] = (uint16_t)pack_bf16(v[j], 0.0f);
     }
   }
 }

@@ -15,6 +15,7 @@
 // the same way whatever the order of the sum, so the codes are reproducible
 // next to the quantizer's borders.
 #include "launch_ops.h"
+#include "pack_bf16.h"
 #include "quant_e4m3.h"
 
 namespace moe {
@@ -42,8 +43,7 @@ __device__ __forceinline__ void load_f32x8(const float* p, float (&f)[8]) {
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(f32_to_bf16(f[0]) | (f32_to_bf16(f[1]) << 16), f32_to_bf16(f[2]) | (f32_to_bf16(f[3]) << 16),
-                    f32_to_bf16(f[4]) | (f32_to_bf16(f[5]) << 16), f32_to_bf16(f[6]) | (f32_to_bf16(f[7]) << 16));
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
 
 // Sum over the 64 lanes, the same bits in every lane.
@@ -53,10 +53,70 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// RES: 0 no residual, 1 bfloat16, 2 float32.  TPR: threads per row.
-template <int RES, int TPR, int CPL>
+// 8 values of h: as bfloat16 where they are (RES: 0 no residual, 1 bfloat16), in
+// float32 with a float32 residual (2).
+template <int RES>
+struct Held {
+  uint4 b;
+  __device__ __forceinline__ void load(const uint16_t* x, const void* residual, size_t base, int c) {
+    b = reinterpret_cast<const uint4*>(x)[c];
+    if constexpr (RES == 1) {
+      float f[8], r[8];
+      unpack8(b, f);
+      unpack8(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(residual) + base)[c], r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] += r[i];
+      b = pack8(f);
+    }
+  }
+  __device__ __forceinline__ void clear() { b = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void store(void* out, size_t base, int c) const {
+    reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + base)[c] = b;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(b, f); }
+  // The compiler would otherwise keep the fp64 values of the sum until the norm.
+  __device__ __forceinline__ void forget() {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("" : "+v"(b.x), "+v"(b.y), "+v"(b.z), "+v"(b.w));
+#endif
+  }
+};
+template <>
+struct Held<2> {
+  float h[8];
+  __device__ __forceinline__ void load(const uint16_t* x, const void* residual, size_t base, int c) {
+    float r[8];
+    unpack8(reinterpret_cast<const uint4*>(x)[c], h);
+    load_f32x8(static_cast<const float*>(residual) + base + 8 * c, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] += r[i];
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = 0.0f;
+  }
+  __device__ __forceinline__ void store(void* out, size_t base, int c) const {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + base + 8 * c);
+    p[0] = make_float4(h[0], h[1], h[2], h[3]);
+    p[1] = make_float4(h[4], h[5], h[6], h[7]);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = h[i];
+  }
+  __device__ __forceinline__ void forget() {
+#ifdef __HIP_DEVICE_COMPILE__
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(h[i]));
+#endif
+  }
+};
+
+// RES as above.  ACT: codes of 0 MXFP4, 1 MXFP8 E4M3, 2 NVFP4, or -1 none.  TPR:
+// threads per row.
+template <int RES, int act, int TPR, int CPL>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) add_rmsnorm_kernel(
-    int act, bool w_f32, int64_t rows, int cols, const uint16_t* x, const void* residual,
+    bool w_f32, int64_t rows, int cols, const uint16_t* x, const void* residual,
     const void* __restrict__ weight, double eps, float g, void* residual_out, uint16_t* y,
     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   constexpr int THREADS = TPR < 256 ? 256 : TPR;
@@ -67,43 +127,24 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) add_rmsnorm_kernel(
   int flip = 0;
   for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < rows; row += (int64_t)gridDim.x * RPB) {
     const size_t base = (size_t)row * cols;
-    float h[CPL][8];
+    Held<RES> h[CPL];
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+      const int c = t + j * TPR;
+      if (c < pieces)
+        h[j].load(x + base, residual, base, c);
+      else
+        h[j].clear();
+    }
     double ss = 0.0;
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
       const int c = t + j * TPR;
-      if (c < pieces) {
-        unpack8(reinterpret_cast<const uint4*>(x + base)[c], h[j]);
-        if constexpr (RES == 1) {
-          float r[8];
-          unpack8(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(residual) + base)[c], r);
+      if (RES != 0 && c < pieces) h[j].store(residual_out, base, c);
+      float v[8];
+      h[j].get(v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[j][i] = bf16_to_f32(f32_to_bf16(h[j][i] + r[i]));
-        } else if constexpr (RES == 2) {
-          float r[8];
-          load_f32x8(static_cast<const float*>(residual) + base + 8 * c, r);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[j][i] += r[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] = 0.0f;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < CPL; ++j) {
-      const int c = t + j * TPR;
-      if constexpr (RES == 1) {
-        if (c < pieces) reinterpret_cast<uint4*>(static_cast<uint16_t*>(residual_out) + base)[c] = pack8(h[j]);
-      } else if constexpr (RES == 2) {
-        if (c < pieces) {
-          float4* p = reinterpret_cast<float4*>(static_cast<float*>(residual_out) + base + 8 * c);
-          p[0] = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
-          p[1] = make_float4(h[j][4], h[j][5], h[j][6], h[j][7]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fma((double)h[j][i], (double)h[j][i], ss);
+      for (int i = 0; i < 8; ++i) ss = fma((double)v[i], (double)v[i], ss);
     }
     ss = wave_sum(ss);
     if constexpr (WPR > 1) {
@@ -116,6 +157,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) add_rmsnorm_kernel(
       flip ^= 1;
     }
     const double rstd = 1.0 / sqrt(ss / cols + eps);
+    if constexpr (CPL >= 4) {
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) h[j].forget();
+    }
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
       const int c = t + j * TPR;
@@ -126,23 +171,27 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) add_rmsnorm_kernel(
         else
           unpack8(static_cast<const uint4*>(weight)[c], w);
       }
-      float n[8];
+      float v[8], n[8];
+      h[j].get(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n[i] = (float)((double)h[j][i] * rstd * (double)w[i]);
+      for (int i = 0; i < 8; ++i) n[i] = (float)((double)v[i] * rstd * (double)w[i]);
       const uint4 yb = pack8(n);
       if (y != nullptr && c < pieces) reinterpret_cast<uint4*>(y + base)[c] = yb;
-      if (act < 0) continue;
+      if constexpr (act >= 0) {
       // The group's absolute maximum on the bit patterns of the rounded y
       // (bf16 magnitudes order as their low 15 bits).
       const uint32_t yw[4] = {yb.x, yb.y, yb.z, yb.w};
-      uint32_t amax = 0;
+      typedef unsigned short v2u16 __attribute__((ext_vector_type(2)));
+      v2u16 m2 = {0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) amax = max(amax, max(yw[i] & 0x7FFFu, (yw[i] >> 16) & 0x7FFFu));
+      for (int i = 0; i < 4; ++i)
+        m2 = __builtin_elementwise_max(m2, __builtin_bit_cast(v2u16, yw[i] & 0x7FFF7FFFu));
+      uint32_t amax = max((uint32_t)m2[0], (uint32_t)m2[1]);
       amax = max(amax, quad_xor<1>(amax));
-      if (act != 2) amax = max(amax, quad_xor<2>(amax));
+      if constexpr (act != 2) amax = max(amax, quad_xor<2>(amax));
       unpack8(yb, n);
       const size_t piece = (size_t)row * pieces + c;   // 8 values each
-      if (act == 1) {
+      if constexpr (act == 1) {
         const int e = mx8_scale_exp(amax << 16);
         const float inv = e4m3_exp2(-e);
         const uint2 q = make_uint2(e4m3_cvt4(n[0], n[1], n[2], n[3], inv), e4m3_cvt4(n[4], n[5], n[6], n[7], inv));
@@ -150,7 +199,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) add_rmsnorm_kernel(
           reinterpret_cast<uint2*>(codes)[piece] = q;
           if (c % 4 == 0) scales[piece / 4] = (uint8_t)(e + 127);
         }
-      } else if (act == 0) {
+      } else if constexpr (act == 0) {
         const int e = mx_scale_exp(amax << 16);
         const float sc = exp2_scale(e);
         uint32_t q = e2m1_pack2<0>(0u, n[0], n[1], sc);
@@ -173,48 +222,55 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) add_rmsnorm_kernel(
           if (c % 2 == 0) scales[piece / 2] = (uint8_t)sc;
         }
       }
+      }
     }
   }
 }
 
 constexpr int64_t kNormMaxBlocks = 1 << 20;   // more rows: a block takes several
 
-template <int RES, int TPR, int CPL>
-hipError_t launch_norm(int act, bool w_f32, int64_t rows, int cols, const uint16_t* x, const void* residual,
-                       const void* weight, float eps, float g, void* residual_out, uint16_t* y, uint8_t* codes,
-                       uint8_t* scales, hipStream_t stream) {
+#define MOE_NORM_PARAMS                                                                                                \
+  bool w_f32, int64_t rows, int cols, const uint16_t *x, const void *residual, const void *weight, float eps, float g, \
+      void *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales, hipStream_t stream
+#define MOE_NORM_ARGS w_f32, rows, cols, x, residual, weight, eps, g, residual_out, y, codes, scales, stream
+
+template <int RES, int ACT, int TPR, int CPL>
+hipError_t launch_norm(MOE_NORM_PARAMS) {
   constexpr int THREADS = TPR < 256 ? 256 : TPR;
   constexpr int RPB = THREADS / TPR;
   const int64_t blocks = (rows + RPB - 1) / RPB;
-  hipLaunchKernelGGL((add_rmsnorm_kernel<RES, TPR, CPL>), dim3((unsigned)(blocks < kNormMaxBlocks ? blocks : kNormMaxBlocks)),
-                     dim3(THREADS), 0, stream, act, w_f32, rows, cols, x, residual, weight, (double)eps, g,
-                     residual_out, y, codes, scales);
+  hipLaunchKernelGGL((add_rmsnorm_kernel<RES, ACT, TPR, CPL>),
+                     dim3((unsigned)(blocks < kNormMaxBlocks ? blocks : kNormMaxBlocks)), dim3(THREADS), 0, stream, w_f32,
+                     rows, cols, x, residual, weight, (double)eps, g, residual_out, y, codes, scales);
   return hipGetLastError();
 }
 
+template <int RES, int ACT>
+hipError_t launch_norm_act(MOE_NORM_PARAMS) {
+  if (cols <= 512) return launch_norm<RES, ACT, 64, 1>(MOE_NORM_ARGS);
+  if (cols <= 1024) return launch_norm<RES, ACT, 64, 2>(MOE_NORM_ARGS);
+  if (cols <= 2048) return launch_norm<RES, ACT, 256, 1>(MOE_NORM_ARGS);
+  if (cols <= 4096) return launch_norm<RES, ACT, 256, 2>(MOE_NORM_ARGS);
+  if (cols <= 8192) return launch_norm<RES, ACT, 256, 4>(MOE_NORM_ARGS);
+  if (cols <= 16384) return launch_norm<RES, ACT, 1024, 2>(MOE_NORM_ARGS);
+  if (cols <= 32768) return launch_norm<RES, ACT, 1024, 4>(MOE_NORM_ARGS);
+  return launch_norm<RES, ACT, 1024, 8>(MOE_NORM_ARGS);
+}
+
 template <int RES>
-hipError_t launch_norm_res(int act, bool w_f32, int64_t rows, int cols, const uint16_t* x, const void* residual,
-                           const void* weight, float eps, float g, void* residual_out, uint16_t* y, uint8_t* codes,
-                           uint8_t* scales, hipStream_t stream) {
-#define MOE_NORM_ARGS act, w_f32, rows, cols, x, residual, weight, eps, g, residual_out, y, codes, scales, stream
-  if (cols <= 512) return launch_norm<RES, 64, 1>(MOE_NORM_ARGS);
-  if (cols <= 1024) return launch_norm<RES, 64, 2>(MOE_NORM_ARGS);
-  if (cols <= 2048) return launch_norm<RES, 256, 1>(MOE_NORM_ARGS);
-  if (cols <= 4096) return launch_norm<RES, 256, 2>(MOE_NORM_ARGS);
-  if (cols <= 8192) return launch_norm<RES, 256, 4>(MOE_NORM_ARGS);
-  if (cols <= 16384) return launch_norm<RES, 1024, 2>(MOE_NORM_ARGS);
-  if (cols <= 32768) return launch_norm<RES, 1024, 4>(MOE_NORM_ARGS);
-  return launch_norm<RES, 1024, 8>(MOE_NORM_ARGS);
-#undef MOE_NORM_ARGS
+hipError_t launch_norm_res(int act, MOE_NORM_PARAMS) {
+  auto f = act == 0 ? launch_norm_act<RES, 0> : act == 1 ? launch_norm_act<RES, 1> : act == 2 ? launch_norm_act<RES, 2>
+                                                                                             : launch_norm_act<RES, -1>;
+  return f(MOE_NORM_ARGS);
 }
 
 }  // namespace
 
-hipError_t launch_add_rmsnorm(int act, bool res_f32, bool w_f32, int64_t rows, int cols, const uint16_t* x,
-                              const void* residual, const void* weight, float eps, float g, void* residual_out,
-                              uint16_t* y, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+hipError_t launch_add_rmsnorm(int act, bool res_f32, MOE_NORM_PARAMS) {
   auto f = residual == nullptr ? launch_norm_res<0> : res_f32 ? launch_norm_res<2> : launch_norm_res<1>;
-  return f(act, w_f32, rows, cols, x, residual, weight, eps, g, residual_out, y, codes, scales, stream);
+  return f(act, MOE_NORM_ARGS);
 }
+#undef MOE_NORM_ARGS
+#undef MOE_NORM_PARAMS
 
 }  // namespace moe

@@ -6,10 +6,13 @@ the library's HIP kernels.  Weights can be loaded either as canonical MXFP4
 moe_w4a4_quantize and then re-laid by moe_w4a4_prepare_weights.  An NVFP4
 layer (MOE_MMA_NVF4_X_NVF4) takes NVFP4 codes, E4M3 scale bytes per 16 and the
 tensor scales instead (moe_w4a4_quantize_nvfp4, moe_w4a4_prepare_weights_nvfp4).
+MoeW4A4Layer.forward_block runs the layer behind its norm and router; W4A4Linear
+is a dense linear on the same formats.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import contextlib
 
 import torch
 
@@ -17,6 +20,8 @@ from . import _lib
 
 
 class MoeW4A4Layer:
+    PREDISPATCH_ROWS = 8192      # routed rows up to which a forward quantizes and routes in one launch
+
     def __init__(self, hidden: int, inter: int, num_experts: int, topk: int, max_tokens: int,
                  device: str | torch.device = "cuda", mma_type: int = _lib.MOE_MMA_MXF4_X_MXF4,
                  prepared: torch.Tensor | None = None):
@@ -136,6 +141,57 @@ class MoeW4A4Layer:
             _lib.moe_w4a4_forward_mega(self.cfg, self.prepared, T, x, topk_ids, topk_weights, out, self.workspace,
                                        stream=stream)
         return out
+
+    # ---- the layer with what feeds it ----------------------------------------
+    def forward_block(self, x, residual, norm_weight, eps, gate_weight, residual_out=None, bias=None,
+                      scoring=_lib.MOE_SCORE_SOFTMAX, num_groups=1, topk_groups=1, renormalize=True, scale=1.0,
+                      shared=None, out=None, stream=None):
+        """One decoder block's feed-forward half: residual addition and norm
+        (moe_w4a4_add_rmsnorm), router logits, the router's choice
+        (moe_w4a4_router), the routed experts, and a shared linear if there is
+        one.  Returns (out, h): out = experts(y) (+ shared(y)) bf16 [T, H], and
+        the new residual stream h = x + residual, of the residual's type.
+        x bf16 [T, H]; residual bf16 / float32 [T, H] (residual_out like it,
+        may be it; a new tensor if None); norm_weight [H]; gate_weight [E, H]
+        bf16 (logits by a plain product), or a W4A4Linear with out_features E;
+        bias float32 [E]; shared: a W4A4Linear from H to H, added to the
+        experts' output before its rounding.  Tokens past the fused
+        pre-dispatch (more than 8192 routed rows) are quantized by the norm,
+        into the workspace, and not read again by a quantizer."""
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"x: {T} tokens, the layer holds {self.max_tokens}")
+        on_stream = torch.cuda.stream(torch.cuda.ExternalStream(int(stream), self.device)) if stream is not None \
+            else contextlib.nullcontext()
+        with torch.cuda.device(self.device), on_stream:
+            if residual_out is None:
+                residual_out = torch.empty_like(residual)
+            if out is None:
+                out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
+            y = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
+            ids = torch.empty((T, self.k), dtype=torch.int32, device=self.device)
+            weights = torch.empty((T, self.k), dtype=torch.float32, device=self.device)
+            codes = scales = None
+            if T * self.k > self.PREDISPATCH_ROWS and not self.nvfp4:
+                wide = self.H if self.mma_type == _lib.MOE_MMA_FP8_X_MXF4 else self.H // 2
+                codes = self.ws("xq", (self.max_tokens, wide), torch.uint8)[:T]
+                scales = self.ws("xsf", (self.max_tokens, self.H // 32), torch.uint8)[:T]
+            _lib.moe_w4a4_add_rmsnorm(x, residual, norm_weight, eps, residual_out=residual_out, y=y, codes=codes,
+                                      scales=scales, mma_type=self.mma_type)
+            if isinstance(gate_weight, W4A4Linear):
+                logits = gate_weight.forward(y, dtype=torch.float32)
+            else:
+                logits = torch.nn.functional.linear(y, gate_weight)
+            _lib.moe_w4a4_router(logits, ids, weights, bias=bias, scoring=scoring, num_groups=num_groups,
+                                 topk_groups=topk_groups, renormalize=renormalize, scale=scale)
+            if codes is None:
+                _lib.moe_w4a4_forward(self.cfg, self.prepared, T, y, ids, weights, out, self.workspace)
+            else:
+                _lib.moe_w4a4_run_stages(self.cfg, self.prepared, T, None, ids, weights, out, self.workspace,
+                                         _lib.MOE_STAGE_ALL & ~_lib.MOE_STAGE_QUANT)
+            if shared is not None:
+                shared.forward(y, out=out, addend=out)
+        return out, residual_out
 
     def run_stages(self, stages, num_tokens, x=None, topk_ids=None, topk_weights=None, out=None,
                    gemm1_acc=None, stream=None):
