@@ -61,18 +61,91 @@ __device__ __forceinline__ void unrolled(F&& f) {
 
 // The wave's outputs acc[token block][row block] to rows t0.. and columns n0..
 // of `out`, G token blocks at a time through `mine` (G*16 x STRIDE bytes of
-// LDS), so that every store covers a whole run of a row: 4*WA lanes a token, 4
-// values a lane.  The loads of a pass's addends are all issued before its
-// first use.  The store loop stays rolled: unrolled over the tokens its code took
-// longer to fetch than to run.
+// LDS), so that every store covers a whole run of a row: V values a lane, 16
+// bytes of `out`.  The loads of a pass's addends are all issued before its first
+// use (one at a time they cost half the kernel's time at 16384 x 4096 outputs).
+// Stores and addend loads are non-temporal: `out` is far larger than an L2, and
+// the operands stay there (16384 x 2048 x 4096 MXFP4 104 -> 80 us).  The store loop
+// stays rolled: unrolled over the tokens its code took longer to fetch than to
+// run.
+template <int WA, int WB, int G, bool F32>
+__device__ __forceinline__ void tile_store(const LinearArgs& p, const uint8_t* mine, int n0, int t0, int live_tokens,
+                                           int lane) {
+  constexpr int STRIDE = WA * 16 * 4 + 16;
+  constexpr int V = F32 ? 4 : 8, LPT = WA * 16 / V, TPP = kWave / LPT, IT = 4;   // lanes a token, tokens a pass, passes in flight
+  const int n = n0 + lane % LPT * V, tl = lane / LPT;
+  const int left = max(0, min(V, p.N - n));
+  const bool whole = p.N % V == 0;                         // then V or none are left, and aligned
+  const int live = left > 0 ? live_tokens : 0;
+#pragma unroll 1
+  for (int i0 = tl; i0 < G * 16; i0 += IT * TPP) {
+    const size_t at = (size_t)(t0 + i0) * p.N + n;
+    v4u add[IT];
+    if (p.addend != nullptr) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        add[i] = v4u{0, 0, 0, 0};
+        if (i0 + i * TPP < live) {
+          const uint16_t* a = p.addend + at + (size_t)(i * TPP) * p.N;
+          if (!whole) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+              if (j < left) add[i][j / 2] |= (uint32_t)a[j] << (j % 2 * 16);
+          } else if constexpr (F32) {
+            const uint64_t q = __builtin_nontemporal_load(reinterpret_cast<const uint64_t*>(a));
+            add[i][0] = (uint32_t)q;
+            add[i][1] = (uint32_t)(q >> 32);
+          } else {
+            add[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(a));
+          }
+        }
+      }
+    }
+    v4f v[IT][V / 4];
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+      for (int h = 0; h < V / 4; ++h)
+        v[i][h] = *reinterpret_cast<const v4f*>(mine + (i0 + i * TPP) * STRIDE + lane % LPT * (V * 4) + h * 16);
+    if (p.addend != nullptr) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j / 4][j % 4] += bf16_to_f32(add[i][j / 2] >> (j % 2 * 16) & 0xFFFFu);
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      if (i0 + i * TPP >= live) continue;
+      if constexpr (F32) {
+        float* o = static_cast<float*>(p.out) + at + (size_t)(i * TPP) * p.N;
+        if (whole) {
+          __builtin_nontemporal_store(v[i][0], reinterpret_cast<v4f*>(o));
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (j < left) o[j] = v[i][0][j];
+        }
+      } else {
+        uint16_t* o = static_cast<uint16_t*>(p.out) + at + (size_t)(i * TPP) * p.N;
+        v4u h;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = pack_bf16(v[i][j / 2][j % 2 * 2], v[i][j / 2][j % 2 * 2 + 1]);
+        if (whole) {
+          __builtin_nontemporal_store(h, reinterpret_cast<v4u*>(o));
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (j < left) o[j] = (uint16_t)(h[j / 2] >> (j % 2 * 16));
+        }
+      }
+    }
+  }
+}
+
 template <int WA, int WB, int G>
 __device__ __forceinline__ void tile_epilogue(const LinearArgs& p, const v4f (&acc)[WB][WA], uint8_t* mine, int n0,
                                               int t0, int lane) {
   constexpr int STRIDE = WA * 16 * 4 + 16;
-  constexpr int LPT = WA * 4, TPP = kWave / LPT, IT = 8;   // lanes a token, tokens a pass, passes in flight
-  const int n = n0 + lane % LPT * 4, tl = lane / LPT;
-  const int left = max(0, min(4, p.N - n));
-  const bool whole = p.N % 4 == 0;                         // then 4 or none are left, and aligned
   unrolled<WB / G>([&](auto qi) {
     constexpr int q = decltype(qi)::value;
 #pragma unroll
@@ -83,68 +156,11 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& p, const v4f (&a
             acc[q * G + c][r];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int live = left > 0 ? p.T - t0 - q * G * 16 : 0;  // tokens of this part that the lane stores
-#pragma unroll 1
-    for (int i0 = tl; i0 < G * 16; i0 += IT * TPP) {
-      const size_t at = (size_t)(t0 + q * G * 16 + i0) * p.N + n;
-      uint2 add[IT];
-      if (p.addend != nullptr) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          add[i] = make_uint2(0, 0);
-          if (i0 + i * TPP < live) {
-            const uint16_t* a = p.addend + at + (size_t)(i * TPP) * p.N;
-            if (whole) {
-              add[i] = *reinterpret_cast<const uint2*>(a);
-            } else {
-              add[i].x = a[0];
-              if (left > 1) add[i].x |= (uint32_t)a[1] << 16;
-              if (left > 2) add[i].y = a[2];
-              if (left > 3) add[i].y |= (uint32_t)a[3] << 16;
-            }
-          }
-        }
-      }
-      v4f v[IT];
-#pragma unroll
-      for (int i = 0; i < IT; ++i)
-        v[i] = *reinterpret_cast<const v4f*>(mine + (i0 + i * TPP) * STRIDE + lane % LPT * 16);
-      if (p.addend != nullptr) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          v[i][0] += bf16_to_f32(add[i].x & 0xFFFFu);
-          v[i][1] += bf16_to_f32(add[i].x >> 16);
-          v[i][2] += bf16_to_f32(add[i].y & 0xFFFFu);
-          v[i][3] += bf16_to_f32(add[i].y >> 16);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        if (i0 + i * TPP >= live) continue;
-        if (p.out_f32) {
-          float* o = static_cast<float*>(p.out) + at + (size_t)(i * TPP) * p.N;
-          if (whole) {
-            *reinterpret_cast<v4f*>(o) = v[i];
-          } else {
-            o[0] = v[i][0];
-            if (left > 1) o[1] = v[i][1];
-            if (left > 2) o[2] = v[i][2];
-            if (left > 3) o[3] = v[i][3];
-          }
-        } else {
-          uint16_t* o = static_cast<uint16_t*>(p.out) + at + (size_t)(i * TPP) * p.N;
-          const uint2 h = make_uint2(pack_bf16(v[i][0], v[i][1]), pack_bf16(v[i][2], v[i][3]));
-          if (whole) {
-            *reinterpret_cast<uint2*>(o) = h;
-          } else {
-            o[0] = (uint16_t)h.x;
-            if (left > 1) o[1] = (uint16_t)(h.x >> 16);
-            if (left > 2) o[2] = (uint16_t)h.y;
-            if (left > 3) o[3] = (uint16_t)(h.y >> 16);
-          }
-        }
-      }
-    }
+    const int t = t0 + q * G * 16;
+    if (p.out_f32)
+      tile_store<WA, WB, G, true>(p, mine, n0, t, p.T - t, lane);
+    else
+      tile_store<WA, WB, G, false>(p, mine, n0, t, p.T - t, lane);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   });
