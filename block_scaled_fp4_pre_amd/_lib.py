@@ -441,7 +441,15 @@ def moe_w4a4_linear(cfg: moe_w4a4_linear_cfg, prepared, x, out, workspace, xq=No
     """out [T, N] (bf16 or float32) = Q(x) W^T (+ addend bf16 [T, N]); x bf16
     [T, K], or None and xq uint8 [T, K/2] (E4M3: [T, K]) with xsf uint8 [T, K/32]."""
     dev = _device_of(out, "out")
-    K, N = cfg.in_features, cfg.out_features
+    pw = _fits(prepared, "prepared", _U8, prepared.shape, dev)
+    pk = _fits(workspace, "workspace", _U8, workspace.shape, dev)
+    _linear_call(ctypes.byref(cfg), cfg.in_features, cfg.out_features, cfg.mma_type, dev, pw, x, out, pk,
+                 workspace.numel(), xq, xsf, addend, stream)
+
+
+def _linear_call(cfg_ref, K: int, N: int, mma_type: int, dev: int, prepared: int, x, out, workspace: int,
+                 workspace_bytes: int, xq, xsf, addend, stream) -> None:
+    """moe_w4a4_linear with the caller's own buffers as addresses (layer.W4A4Linear)."""
     px = pq = ps = pa = None
     if x is not None:
         if xq is not None or xsf is not None:
@@ -452,14 +460,12 @@ def moe_w4a4_linear(cfg: moe_w4a4_linear_cfg, prepared, x, out, workspace, xq=No
         if xq is None or xsf is None:
             raise ValueError("either x, or xq and xsf")
         T = xq.shape[0] if xq.dim() == 2 else -1
-        pq = _fits(xq, "xq", _U8, (T, K if cfg.mma_type == MOE_MMA_FP8_X_MXF4 else K // 2), dev)
+        pq = _fits(xq, "xq", _U8, (T, K if mma_type == MOE_MMA_FP8_X_MXF4 else K // 2), dev)
         ps = _fits(xsf, "xsf", _U8, (T, K // 32), dev)
     if addend is not None:
         pa = _fits(addend, "addend", _BF16, (T, N), dev)
     po = _fits(out, "out", _BF16_F32, (T, N), dev)
-    pw = _fits(prepared, "prepared", _U8, prepared.shape, dev)
-    pk = _fits(workspace, "workspace", _U8, workspace.shape, dev)
-    st = _lib.moe_w4a4_linear(ctypes.byref(cfg), pw, T, px, pq, ps, pa, 1 if out.dtype is torch.float32 else 0, po, pk,
-                              workspace.numel(), _raw_stream(stream, dev))
+    st = _lib.moe_w4a4_linear(cfg_ref, prepared, T, px, pq, ps, pa, 1 if out.dtype is torch.float32 else 0, po,
+                              workspace, workspace_bytes, _raw_stream(stream, dev))
     if st != MOE_OK:
         raise MoeError(st, "moe_w4a4_linear")

@@ -41,26 +41,36 @@ struct LinearInput {
   int T, K;
 };
 
-// Which kernel takes a product, from its number of 128 x 128 tiles.  Below 128
-// (half the CUs) the split kernel, whose tiles are smaller and whose waves share
-// the K steps; from 128 on the tile kernel, with tiles of 256 rows x 128 tokens
-// once those give every CU the two workgroups it holds.  Measured with K = 4096
-// (split / 128 / 256 rows), MXFP4: 256 x 4096 outputs 8.8 / 13.6 / 21 us, 512 x 4096
-// 15.0 / 14.2 / 22, 64 x 32000 18.6 / 15.8 / 22, 2048 x 4096 58 / 23.9 / 25.1, 4096 x 4096
-// 119 / 41 / 38; E4M3: 512 x 4096 19.1 / 17.6 / 32, 4096 x 4096 - / 55.7 / 54.7.
+// Which kernel takes a product.  Measured with K = 4096 and N = 4096 unless said
+// otherwise, MXFP4 (E4M3), us of the product's kernel:
+//   tokens        split        64 tokens    128 tokens   256 rows
+//                              2 groups                  128 tokens
+//   128           6.0 (7.4)    9.1 (10.8)   13 (16)      20 (30)
+//   256           8.6 (10.6)   9.5 (11.4)   13.6 (16)    21 (30)
+//   512           15.2 (18.9)  10.3 (13.0)  14.0 (16.5)  22 (31)
+//   1024          26 (35)      18.6 (22.2)  16 (18.6)    22 (32)
+//   2048          57 (87)      34 (42)      22.3 (29.5)  25 (35)
+//   4096          119 (-)      -            41 (55.7)    37.6 (54.7)
+//   64, N 32000   18.6         14.5         15.2         22
+//   256, K 16384, N 2048: 13.1 / 23 / 36 / 58
+// So, by the number of tiles: the split kernel, whose tiles are smaller and whose
+// waves share the K steps, up to 128 tiles of 128 rows x 64 tokens (half the CUs);
+// those with two groups of waves up to one a CU; tiles of 128 x 128, two a CU; and
+// of 256 rows x 128 tokens once these give every CU its two.
 // Up to kDecodeMaxTokens tokens and kDecodeMaxSteps K steps: the decode kernel,
 // which needs no tokens in tile order.
 constexpr int kDecodeMaxTokens = 16, kDecodeMaxSteps = 64;
-enum LinearPlan { kLinearDecode, kLinearSplit, kLinearTile128, kLinearTile256 };
+enum LinearPlan { kLinearDecode, kLinearSplit, kLinearTile64, kLinearTile128, kLinearTile256 };
 inline LinearPlan linear_plan(int T, int N, int steps) {
   if (T <= kDecodeMaxTokens && steps <= kDecodeMaxSteps) return kLinearDecode;
-  const int64_t tt = (T + 127) / 128;
-  if (tt * ((N + 127) / 128) < 128) return kLinearSplit;
-  return tt * ((N + 255) / 256) >= 512 ? kLinearTile256 : kLinearTile128;
+  const int64_t t64 = (T + 63) / 64, t128 = (T + 127) / 128, n128 = (N + 127) / 128, n256 = (N + 255) / 256;
+  if (t64 * n128 <= 128) return kLinearSplit;
+  if (t64 * n128 <= 256) return kLinearTile64;
+  return t128 * n256 >= 512 ? kLinearTile256 : kLinearTile128;
 }
 // Units of 64 tokens that the plan's kernel reads: whole tiles.
 inline int linear_token_units(LinearPlan plan, int T) {
-  return plan == kLinearSplit ? (T + 63) / 64 : (T + 127) / 128 * 2;
+  return plan == kLinearSplit || plan == kLinearTile64 ? (T + 63) / 64 : (T + 127) / 128 * 2;
 }
 hipError_t launch_linear_decode(bool fp8, const LinearArgs& a, const LinearInput& in, hipStream_t stream);   // linear_decode.hip
 hipError_t launch_linear_split(bool fp8, const LinearArgs& a, hipStream_t stream);              // linear.hip

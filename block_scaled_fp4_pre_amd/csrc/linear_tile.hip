@@ -12,6 +12,10 @@
 // the compiler cannot tell the ring's stages apart and would wait for all of them
 // before every LDS read.  Reads and DMAs are issued between the step's MFMAs, and
 // two workgroups share a CU, so that one's MFMAs cover the other's waits.
+//
+// KS = 2, for products with too few tiles for that: two groups of 4 waves share a
+// tile, each with a ring of its own and every other K step, and exchange half of
+// their sums at the end (group 0 finishes the first half of the tokens).
 #include "linear_common.h"
 
 namespace moe {
@@ -45,6 +49,7 @@ struct TileShape {
   static constexpr int DMAS = AD + BD + SD;
   static constexpr int ROWS = AB * 16, TOKENS = BB * 16;
   static_assert(AD * WAVES == AB && BD * WAVES == BB * (TB / 1024) && AB % 4 == 0 && BB % 4 == 0, "DMA shares");
+  static_assert(WA % 4 == 0 && (WB % 4 == 0 || WB == 2), "scale dwords");
 };
 
 template <int N>
@@ -72,7 +77,9 @@ template <int WA, int WB, int G, bool F32>
 __device__ __forceinline__ void tile_store(const LinearArgs& p, const uint8_t* mine, int n0, int t0, int live_tokens,
                                            int lane) {
   constexpr int STRIDE = WA * 16 * 4 + 16;
-  constexpr int V = F32 ? 4 : 8, LPT = WA * 16 / V, TPP = kWave / LPT, IT = 4;   // lanes a token, tokens a pass, passes in flight
+  constexpr int V = F32 ? 4 : 8, LPT = WA * 16 / V, TPP = kWave / LPT;   // lanes a token, tokens a pass
+  constexpr int IT = G * 16 / TPP < 4 ? G * 16 / TPP : 4;                // passes in flight
+  static_assert(G * 16 % (IT * TPP) == 0, "whole passes");
   const int n = n0 + lane % LPT * V, tl = lane / LPT;
   const int left = max(0, min(V, p.N - n));
   const bool whole = p.N % V == 0;                         // then V or none are left, and aligned
@@ -166,12 +173,14 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& p, const v4f (&a
   });
 }
 
-template <bool F8, int WA, int WB, int P>
-__global__ void __launch_bounds__(64 * kTileWaves, 2) linear_tile_kernel(LinearArgs p, int row_tiles, int tok_tiles) {
+template <bool F8, int WA, int WB, int P, int KS>
+__global__ void __launch_bounds__(64 * kTileWaves * KS, 2) linear_tile_kernel(LinearArgs p, int row_tiles, int tok_tiles) {
   using S = TileShape<F8, WA, WB>;
   constexpr int TB = S::TB;
   extern __shared__ __align__(16) uint8_t lds[];
-  const uint32_t lbase = (uint32_t)(uintptr_t)lds;
+  const int group = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * kTileWaves));
+  const uint8_t* ring = lds + group * (P * S::BYTES);
+  const uint32_t lbase = (uint32_t)(uintptr_t)ring;
   // Workgroups are dealt round-robin to the 8 XCDs; each XCD gets a run of the
   // order below (4 row tiles wide, tokens next), so that the tiles it works on
   // at a time share their operands in its L2.
@@ -180,7 +189,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) linear_tile_kernel(LinearA
   const int band = L / (4 * tok_tiles), width = min(4, row_tiles - band * 4);
   const int in = L - band * 4 * tok_tiles, tt = in / width, rt = band * 4 + in - tt * width;
   const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave % kTileWaves);   // in its group
   const int wr = wave & 1, wt = wave >> 1;              // the wave's half of the rows, of the tokens
   const int S_ = p.steps;
 
@@ -212,7 +221,8 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) linear_tile_kernel(LinearA
   };
   // Past the last step the DMAs copy the last stage again (out of L2) into a
   // buffer that is not read any more, so that every step has as many in flight.
-  auto source = [&](int s) { return min(s, S_ - 1); };
+  // The group's step s is step s * KS + group of the product.
+  auto source = [&](int s) { return min(s * KS + group, S_ - 1); };
 #pragma unroll 1
   for (int s = 0; s < P - 1; ++s)
     for (int i = 0; i < S::DMAS; ++i) dma(source(s), s, i);
@@ -222,18 +232,20 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) linear_tile_kernel(LinearA
   for (int c = 0; c < WB; ++c)
 #pragma unroll
     for (int r = 0; r < WA; ++r) acc[c][r] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int s = 0, buf = 0; s < S_; ++s) {
+  for (int s = 0, buf = 0; s * KS < S_; ++s) {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::DMAS * (P - 2)) : "memory");
-    const uint8_t* st = lds + buf * S::BYTES;
+    if (KS > 1 && s * KS + group >= S_) break;    // (an odd number of steps: group 1's last)
+    const uint8_t* st = ring + buf * S::BYTES;
     const int src = source(s + P - 1), dst = buf == 0 ? P - 1 : buf - 1;
     v4u a[WA], b[WB], b2[F8 ? WB : 1];
-    int sa[WA / 4], sb[WB / 4];
+    int sa[WA / 4], sb[(WB + 3) / 4];
 #pragma unroll
     for (int u = 0; u < WA / 4; ++u)
       sa[u] = *reinterpret_cast<const int*>(st + S::A_SCALES + (wr * (WA / 4) + u) * kStepScaleBytes + lane * 4);
 #pragma unroll
-    for (int u = 0; u < WB / 4; ++u)
-      sb[u] = *reinterpret_cast<const int*>(st + S::B_SCALES + (wt * (WB / 4) + u) * kStepScaleBytes + lane * 4);
+    for (int u = 0; u < (WB + 3) / 4; ++u)
+      sb[u] = (int)(*reinterpret_cast<const uint32_t*>(st + S::B_SCALES + (wt * WB / 4 + u) * kStepScaleBytes + lane * 4) >>
+                    (wt * WB % 4 * 8));      // (two blocks a wave: its half of the dword)
     auto read_b = [&](int c) {
       const uint8_t* q = st + S::B_CODES + (wt * WB + c) * TB + lane * 16;
       b[c] = *reinterpret_cast<const v4u*>(q);
@@ -260,34 +272,66 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) linear_tile_kernel(LinearA
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 
-  constexpr int STRIDE = WA * 16 * 4 + 16, G = S::WAVES * 64 * STRIDE <= P * S::BYTES ? 4 : 2;
-  static_assert(S::WAVES * G * 16 * STRIDE <= P * S::BYTES, "epilogue staging");
-  __syncthreads();                          // every wave is done with the ring
-  tile_epilogue<WA, WB, G>(p, acc, lds + wave * G * 16 * STRIDE, rt * S::ROWS + wr * WA * 16,
-                           tt * S::TOKENS + wt * WB * 16, lane);
+  __syncthreads();                          // every wave is done with the rings
+  constexpr int STRIDE = WA * 16 * 4 + 16;
+  const int n0 = rt * S::ROWS + wr * WA * 16, t0 = tt * S::TOKENS + wt * WB * 16;
+  if constexpr (KS == 1) {
+    constexpr int G = S::WAVES * 64 * STRIDE <= P * S::BYTES ? 4 : 2;
+    static_assert(S::WAVES * G * 16 * STRIDE <= P * S::BYTES, "epilogue staging");
+    tile_epilogue<WA, WB, G>(p, acc, lds + wave * G * 16 * STRIDE, n0, t0, lane);
+  } else {
+    constexpr int HALF = WB / 2;
+    static_assert(KS == 2 && 2 * S::WAVES * HALF * WA * 1024 <= KS * P * S::BYTES, "exchange");
+    static_assert(2 * S::WAVES * (HALF * WA * 1024 + 16 * STRIDE) <= KS * P * S::BYTES, "epilogue staging");
+    v4f* red = reinterpret_cast<v4f*>(lds) + wave * HALF * WA * kWave + lane;
+    constexpr int OTHER = S::WAVES * HALF * WA * kWave;
+#pragma unroll
+    for (int c = 0; c < HALF; ++c)
+#pragma unroll
+      for (int r = 0; r < WA; ++r) {
+        if (group == 0)
+          red[(c * WA + r) * kWave] = acc[HALF + c][r];
+        else
+          red[OTHER + (c * WA + r) * kWave] = acc[c][r];
+      }
+    __syncthreads();
+    v4f fin[HALF][WA];
+#pragma unroll
+    for (int c = 0; c < HALF; ++c)
+#pragma unroll
+      for (int r = 0; r < WA; ++r)
+        fin[c][r] = group == 0 ? acc[c][r] + red[OTHER + (c * WA + r) * kWave]
+                               : red[(c * WA + r) * kWave] + acc[HALF + c][r];
+    // staged behind the exchanged sums, which other waves may still read
+    tile_epilogue<WA, HALF, 1>(p, fin, lds + 2 * OTHER * sizeof(v4f) + (group * S::WAVES + wave) * 16 * STRIDE, n0,
+                               t0 + group * HALF * 16, lane);
+  }
 }
 
-template <bool F8, int WA, int WB, int P>
+template <bool F8, int WA, int WB, int P, int KS>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
   using S = TileShape<F8, WA, WB>;
   const int64_t rt = (a.N + S::ROWS - 1) / S::ROWS, tt = (a.T + S::TOKENS - 1) / S::TOKENS;
-  auto kern = linear_tile_kernel<F8, WA, WB, P>;
-  const size_t lds = (size_t)P * S::BYTES;
-  static_assert(2 * P * S::BYTES <= 160 * 1024, "two workgroups a CU");
+  auto kern = linear_tile_kernel<F8, WA, WB, P, KS>;
+  const size_t lds = (size_t)KS * P * S::BYTES;
+  static_assert(2 * P * S::BYTES <= 160 * 1024, "two rings a CU");
   const hipError_t err = raise_lds_limit(reinterpret_cast<const void*>(kern), lds);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(kern, dim3((unsigned)((rt * tt + 7) / 8 * 8)), dim3(64 * S::WAVES), lds, stream, a, (int)rt,
+  hipLaunchKernelGGL(kern, dim3((unsigned)((rt * tt + 7) / 8 * 8)), dim3(64 * S::WAVES * KS), lds, stream, a, (int)rt,
                      (int)tt);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// E4M3 tokens double a stage's token bytes: two stages, still two workgroups a CU.
+// E4M3 tokens double a stage's token bytes: fewer stages, still two rings a CU.
 hipError_t launch_linear_tile(bool fp8, LinearPlan plan, const LinearArgs& a, hipStream_t stream) {
-  if (plan == kLinearTile256)
-    return fp8 ? launch_tile<true, 8, 4, 2>(a, stream) : launch_tile<false, 8, 4, 3>(a, stream);
-  return fp8 ? launch_tile<true, 4, 4, 3>(a, stream) : launch_tile<false, 4, 4, 4>(a, stream);
+  switch (plan) {
+    case kLinearTile256: return fp8 ? launch_tile<true, 8, 4, 2, 1>(a, stream) : launch_tile<false, 8, 4, 3, 1>(a, stream);
+    case kLinearTile128: return fp8 ? launch_tile<true, 4, 4, 3, 1>(a, stream) : launch_tile<false, 4, 4, 4, 1>(a, stream);
+    case kLinearTile64: return fp8 ? launch_tile<true, 4, 2, 4, 2>(a, stream) : launch_tile<false, 4, 2, 4, 2>(a, stream);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace moe

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import contextlib
+import ctypes
 
 import torch
 
@@ -221,6 +222,8 @@ class W4A4Linear:
         linear of the same shape to share (see with_capacity)."""
         self.K, self.N, self.max_tokens, self.mma_type = in_features, out_features, max_tokens, mma_type
         self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError(f"expected a GPU, got {self.device}")
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.cfg = _lib.make_linear_cfg(in_features, out_features, max_tokens, mma_type)
@@ -231,6 +234,7 @@ class W4A4Linear:
             raise ValueError("shared prepared buffer is too small or on another device")
         self.prepared = prepared
         self.workspace = torch.empty(max(wb, 1), dtype=torch.uint8, device=self.device)
+        self._cfg_ref, self._workspace_bytes = ctypes.byref(self.cfg), wb
 
     def with_capacity(self, max_tokens: int, mma_type: int | None = None) -> "W4A4Linear":
         """A linear over the same prepared weights with its own workspace."""
@@ -255,11 +259,12 @@ class W4A4Linear:
         if out is None:
             T = (x if x is not None else xq).shape[0]
             out = torch.empty((T, self.N), dtype=dtype, device=self.device)
-        if torch.cuda.current_device() == self.device.index:
-            _lib.moe_w4a4_linear(self.cfg, self.prepared, x, out, self.workspace, xq, xsf, addend, stream)
-        else:
-            with torch.cuda.device(self.device):
-                _lib.moe_w4a4_linear(self.cfg, self.prepared, x, out, self.workspace, xq, xsf, addend, stream)
+        index = self.device.index
+        if torch._C._cuda_getDevice() != index:
+            with torch.cuda.device(index):
+                return self._run(x, xq, xsf, out, addend, dtype, stream)
+        _lib._linear_call(self._cfg_ref, self.K, self.N, self.mma_type, index, self.prepared.data_ptr(), x, out,
+                          self.workspace.data_ptr(), self._workspace_bytes, xq, xsf, addend, stream)
         return out
 
     def forward(self, x, out=None, addend=None, dtype=torch.bfloat16, stream=None):

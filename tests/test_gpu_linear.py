@@ -158,3 +158,32 @@ def test_repeats_give_the_same_bits(mma):
         first = lin.forward(dev_bf16(x))
         for _ in range(5):
             assert torch.equal(lin.forward(dev_bf16(x)), first)
+
+
+# what launch_ops.h's linear_plan sends to each tile kernel, ragged on every side
+TILED = [(500, 288, 3001, "64 tokens"), (257, 32, 4096, "64 tokens"), (70, 1056, 10000, "64 tokens"),
+         (1100, 160, 2050, "128 tokens"), (70, 416, 20001, "128 tokens"), (2000, 640, 2048, "128 tokens"),
+         (4100, 96, 4097, "256 rows"), (16000, 416, 1030, "256 rows"), (300, 288, 50000, "256 rows")]
+
+
+@TYPES
+@pytest.mark.parametrize("T,K,N,plan", TILED, ids=lambda v: str(v))
+def test_tile_kernels(T, K, N, plan, mma):
+    t64, t128, n128, n256 = -(-T // 64), -(-T // 128), -(-N // 128), -(-N // 256)
+    assert plan == ("64 tokens" if 128 < t64 * n128 <= 256 else "256 rows" if t128 * n256 >= 512 else "128 tokens")
+    log(f"[test] linear T {T} K {K} N {N} mma {mma}: {plan}")
+    x, (wc, ws), add = tokens(T, K, 20), weights(N, K, 21), tokens(T, N, 22)
+    lin = make_linear(K, N, T, mma, wc, ws)
+    c, s, ref, mag = reference(x, wc, ws, mma)
+    got = run(lin, x, T, N)
+    close(got.double().cpu().numpy(), ref, mag, K, mma)
+    assert torch.equal(run(lin, x, T, N, quantized=(c, s)), got)
+    f32 = run(lin, x, T, N, dtype=torch.float32)
+    close(f32.double().cpu().numpy(), ref, mag, K, mma, f32=True)
+    a = bf16.decode(add)
+    plus = run(lin, x, T, N, addend=dev_bf16(add))
+    close(plus.double().cpu().numpy(), ref + a, mag + np.abs(a), K, mma)
+    plus32 = run(lin, x, T, N, dtype=torch.float32, addend=dev_bf16(add))
+    assert torch.equal(plus32.to(torch.bfloat16), plus)
+    again = run(lin, x, T, N)
+    assert torch.equal(again, got)

@@ -33,7 +33,7 @@ def kernels(tmp_path_factory):
         found[m.group(1)] = text[m.end():text.find("s_endpgm", m.end())]
     scratch = dict(re.findall(r"\.name:\s+(_ZN3moe\w*linear_tile_kernel\w*)\n(?:.*\n)*?\s+\.private_segment_fixed_size:\s+(\d+)",
                               text))
-    assert len(found) == 4
+    assert found, "no tile kernels in the assembly"
     return found, scratch
 
 
