@@ -63,6 +63,14 @@ __device__ __forceinline__ float wave_sum(float v) {
   v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x143, 0xC, 0xF, false));
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
+// Sum of lanes 0 to 15.
+__device__ __forceinline__ float row_sum(float v) {
+  v += __uint_as_float(dpp<0x111>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<0x112>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<0x114>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<0x118>(__float_as_uint(v)));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 15));
+}
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int m = 1; m < kWave; m <<= 1) v += __shfl_xor(v, m);
@@ -140,7 +148,8 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(
         rsum = wave_sum(s);
       }
     }
-    int mine = -1;                         // lane j: the expert of slot j
+    int mine = -1;                         // lane j: the expert of slot j, and its logit
+    float logit = 0.0f;
     for (bool exact = !BIAS;; exact = true) {
       uint32_t key[EPL];
       float unsure = 0.0f;                 // more than two keys' values can be closer than they look
@@ -156,7 +165,8 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(
         for (int i = 0; i < EPL; ++i) {
           key[i] = 0;
           if (order_key(l[i])) {
-            const float s = score32(scoring, l[i], top) / rsum, c = s + b[i];
+            const float q = score32(scoring, l[i], top);
+            const float s = scoring == MOE_SCORE_SOFTMAX ? q / rsum : q, c = s + b[i];
             key[i] = order_key(c);
             if (key[i]) big = fmaxf(big, fmaxf(s, fabsf(c)));
           }
@@ -224,11 +234,13 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(
       float last = 0.0f;
       for (int j = 0; j < k + (exact ? 0 : 1); ++j) {
         uint32_t best = key[0];
+        float val = l[0];
         int at = lane;
 #pragma unroll
         for (int i = 1; i < EPL; ++i)
           if (key[i] > best) {
             best = key[i];
+            val = l[i];
             at = i * kWave + lane;
           }
         const uint32_t m = wave_max(best);
@@ -238,10 +250,19 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(
           last = key_value(m);
         }
         uint64_t tied = __ballot(best == m);
-        int e = __builtin_amdgcn_readlane(at, (int)__builtin_ctzll(tied));
-        for (tied &= tied - 1; tied; tied &= tied - 1)
-          e = min(e, __builtin_amdgcn_readlane(at, (int)__builtin_ctzll(tied)));
-        if (j < k && lane == j) mine = e;
+        int owner = (int)__builtin_ctzll(tied), e = __builtin_amdgcn_readlane(at, owner);
+        for (tied &= tied - 1; tied; tied &= tied - 1) {
+          const int o = (int)__builtin_ctzll(tied), e2 = __builtin_amdgcn_readlane(at, o);
+          if (e2 < e) {
+            e = e2;
+            owner = o;
+          }
+        }
+        const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(val), owner));
+        if (j < k && lane == j) {
+          mine = e;
+          logit = v;
+        }
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
           if (i * kWave + lane == e) key[i] = 0;
@@ -249,13 +270,8 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(
       if (exact || sure) break;
     }
     float s = 0.0f;
-    if (mine >= 0) s = score32(scoring, load_logit(bf16, logits, t * E + mine), top) / rsum;
-    if (renormalize) {
-      float sum = s;                       // lanes from k on hold 0
-#pragma unroll
-      for (int m = 1; m < 16; m <<= 1) sum += __shfl_xor(sum, m);
-      s = s / (sum + 1e-20f);
-    }
+    if (mine >= 0) s = scoring == MOE_SCORE_SOFTMAX ? score32(scoring, logit, top) / rsum : score32(scoring, logit, top);
+    if (renormalize) s = s / (row_sum(s) + 1e-20f);        // lanes from k on hold 0
     if (lane < k) {
       ids[t * k + lane] = mine;
       weights[t * k + lane] = s * scale;
