@@ -187,3 +187,84 @@ def test_tile_kernels(T, K, N, plan, mma):
     assert torch.equal(plus32.to(torch.bfloat16), plus)
     again = run(lin, x, T, N)
     assert torch.equal(again, got)
+
+
+@TYPES
+@pytest.mark.parametrize("T,K,N", [(4, 8192, 100), (16, 8192, 64), (16, 8160, 33), (3, 8224, 70), (16, 16384, 48),
+                                   (2, 65536, 33), (40, 65536, 20)])
+def test_long_rows(T, K, N, mma):
+    """Up to and past what the decode kernel holds in LDS (64 K steps), and the longest K."""
+    log(f"[test] linear T {T} K {K} N {N} mma {mma}")
+    x, (wc, ws) = tokens(T, K, 23), weights(N, K, 24)
+    lin = make_linear(K, N, T, mma, wc, ws)
+    c, s, ref, mag = reference(x, wc, ws, mma)
+    got = run(lin, x, T, N)
+    close(got.double().cpu().numpy(), ref, mag, K, mma)
+    assert torch.equal(run(lin, x, T, N, quantized=(c, s)), got)
+
+
+@TYPES
+@pytest.mark.parametrize("T", [5, 70, 1100])
+def test_a_token_that_is_not_finite_leaves_the_others_alone(T, mma):
+    log(f"[test] linear with non-finite tokens T {T} mma {mma}")
+    K, N = 256, 2050
+    x, (wc, ws) = tokens(T, K, 25), weights(N, K, 26)
+    lin = make_linear(K, N, T, mma, wc, ws)
+    clean = run(lin, x, T, N)
+    bad = x.copy()
+    bad[1, 7], bad[3, 200] = 0x7FC0, 0x7F80
+    got = run(lin, bad, T, N)
+    keep = [t for t in range(T) if t not in (1, 3)]
+    assert torch.equal(got[keep], clean[keep])
+
+
+def test_offsets_past_32_bits():
+    """Tokens of more than 2^32 bytes, and weights of more than 2^32 bytes of
+    codes: the last tokens and rows against the oracle."""
+    log("[test] linear with offsets past 32 bits")
+    T, K, N = 600_001, 4096, 24
+    wc, ws = weights(N, K, 27)
+    lin = make_linear(K, N, T, FP8, wc, ws)
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
+    tail = tokens(70, K, 28)
+    x[-70:] = dev_bf16(tail)
+    out = lin.forward(x)
+    _, _, ref, mag = reference(tail, wc, ws, FP8)
+    close(out[-70:].double().cpu().numpy(), ref, mag, K, FP8)
+    assert torch.count_nonzero(out[:-70]).item() == 0
+    del x, out, lin
+    K, N = 16384, 600_003
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((N, K // 32), 120, dtype=torch.uint8, device="cuda")
+    wc, ws = weights(40, K, 29)
+    codes[-40:], scales[-40:] = dev(wc), dev(ws)
+    lin = W4A4Linear(K, N, 20, mma_type=MX4)
+    lin.load_canonical(codes, scales)
+    for T in (2, 20):
+        x = tokens(T, K, 30)
+        out = lin.forward(dev_bf16(x))
+        _, _, ref, mag = reference(x, wc, ws, MX4)
+        close(out[:, -40:].double().cpu().numpy(), ref, mag, K, MX4)
+        assert torch.count_nonzero(out[:, :-40]).item() == 0
+
+
+@TYPES
+def test_first_call_of_a_kernel_inside_a_capture(mma):
+    """A call whose launch limits were not raised before is captured, replayed
+    and equals the eager call."""
+    log(f"[test] linear captured first, mma {mma}")
+    K, N = 8192, 128
+    wc, ws = weights(N, K, 31)
+    lin = make_linear(K, N, 16, mma, wc, ws)
+    x = dev_bf16(tokens(16, K, 32))
+    out = torch.zeros((16, N), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lin.forward(x, out=out)
+    for seed in (33, 34, 35):
+        x.copy_(dev_bf16(tokens(16, K, seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, lin.forward(x))

@@ -157,3 +157,46 @@ def test_no_rows_and_equals_the_layers_own_quantizer():
     _lib.moe_w4a4_quantize(y, c2, s2)
     torch.cuda.synchronize()
     assert torch.equal(c, c2) and torch.equal(s, s2)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values in all: the last rows against the oracle."""
+    log("[test] norm with offsets past 32 bits")
+    rows, cols = 524_299, 4096
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    tail = make(9, cols, 14)
+    x[-9:] = dev_bf16(tail)
+    y = torch.empty_like(x)
+    codes = torch.empty((rows, cols), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device="cuda")
+    _lib.moe_w4a4_add_rmsnorm(x, None, torch.ones(cols, device="cuda"), EPS, y=y, codes=codes, scales=scales, mma_type=FP8)
+    torch.cuda.synchronize()
+    n, d = norm.rmsnorm(bf16.decode(tail), np.ones(cols), EPS), (cols + 8) * 2.0 ** -53
+    got = host_bits(y[-9:])
+    assert np.all((got == norm.round_y(n * (1 - d))) | (got == norm.round_y(n * (1 + d))))
+    c, s = mxfp8.quantize_packed(bf16.decode(got))
+    assert np.array_equal(codes[-9:].cpu().numpy(), c) and np.array_equal(scales[-9:].cpu().numpy(), s)
+    assert torch.count_nonzero(y[:-9]).item() == 0 and torch.count_nonzero(codes[:-9]).item() == 0
+
+
+@pytest.mark.parametrize("cols", [512, 4096, 65536])
+def test_captured_and_replayed(cols):
+    log(f"[test] norm captured, cols {cols}")
+    x, r = (dev_bf16(make(3, cols, s)) for s in (15, 16))
+    w = torch.ones(cols, device="cuda")
+    y, ro = torch.empty_like(x), torch.empty_like(r)
+    c, s = torch.empty((3, cols // 2), dtype=torch.uint8, device="cuda"), \
+        torch.empty((3, cols // 32), dtype=torch.uint8, device="cuda")
+    call = lambda: _lib.moe_w4a4_add_rmsnorm(x, r, w, EPS, residual_out=ro, y=y, codes=c, scales=s, mma_type=MX4)  # noqa: E731
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for seed in (17, 18, 19):
+        x.copy_(dev_bf16(make(3, cols, seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (y, ro, c, s)]
+        call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (y, ro, c, s)))

@@ -144,3 +144,49 @@ def test_no_tokens():
     _lib.moe_w4a4_router(torch.empty((0, 16), device="cuda"), torch.empty((0, 2), dtype=torch.int32, device="cuda"),
                          torch.empty((0, 2), device="cuda"))
     torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the last tokens against the oracle."""
+    log("[test] router with offsets past 32 bits")
+    T, E = 8_400_003, 257
+    logits = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    tail = bf16.decode(bf16.encode(np.random.default_rng(4).normal(size=(21, E))))
+    logits[-21:] = torch.from_numpy(tail).to(torch.bfloat16)
+    ids = torch.empty((T, 5), dtype=torch.int32, device="cuda")
+    w = torch.empty((T, 5), device="cuda")
+    _lib.moe_w4a4_router(logits, ids, w)
+    torch.cuda.synchronize()
+    rid, rw = router.route_logits(tail, 5, "softmax")
+    assert np.array_equal(ids[-21:].cpu().numpy(), rid)
+    assert np.allclose(w[-21:].cpu().numpy(), rw, rtol=2.0 ** -18)
+    assert torch.equal(ids[:-21], torch.arange(5, dtype=torch.int32, device="cuda").expand(T - 21, 5))
+
+
+@pytest.mark.parametrize("scale", [0.0, -2.5])
+def test_scale_of_any_sign(scale):
+    log(f"[test] router scale {scale}")
+    x = np.random.default_rng(5).normal(size=(7, 40))
+    x[3, 2:] = -math.inf
+    check(x, 4, "sigmoid", scale=scale)
+    check(x, 4, "softmax", bias=np.zeros(40, np.float32), groups=5, keep=2, scale=scale, renorm=False)
+
+
+def test_captured_and_replayed():
+    log("[test] router captured")
+    l, b = torch.randn((33, 160), device="cuda"), torch.randn(160, device="cuda") * 0.1
+    ids, w = torch.empty((33, 8), dtype=torch.int32, device="cuda"), torch.empty((33, 8), device="cuda")
+    call = lambda: _lib.moe_w4a4_router(l, ids, w, bias=b, scoring=SCORING["sqrtsoftplus"], num_groups=8,  # noqa: E731
+                                        topk_groups=3)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        l.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = ids.clone(), w.clone()
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], ids) and torch.equal(got[1], w)
