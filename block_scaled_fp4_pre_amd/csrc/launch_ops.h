@@ -45,8 +45,8 @@ struct LinearInput {
 // otherwise, MXFP4 (E4M3), us of the product's kernel:
 //   tokens        split        64 tokens    128 tokens   256 rows
 //                              2 groups                  128 tokens
-//   128           6.0 (7.4)    9.1 (10.8)   13 (16)      20 (30)
-//   256           8.6 (10.6)   9.5 (11.4)   13.6 (16)    21 (30)
+//   128           5.6 (7.4)    9.1 (10.8)   13 (16)      20 (30)
+//   256           8.4 (10.6)   9.5 (11.4)   13.6 (16)    21 (30)
 //   512           15.2 (18.9)  10.3 (13.0)  14.0 (16.5)  22 (31)
 //   1024          26 (35)      18.6 (22.2)  16 (18.6)    22 (32)
 //   2048          57 (87)      34 (42)      22.3 (29.5)  25 (35)

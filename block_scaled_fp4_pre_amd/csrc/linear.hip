@@ -5,7 +5,9 @@
 // linear_split_kernel: a workgroup of 8 waves owns NR*16 weight rows x NT*16
 // tokens; its waves split the K steps (wave w takes w, w + 8, ...), each with
 // the whole tile in its accumulators, and their sums meet in LDS, added in wave
-// order.
+// order.  The next step's operands are loaded before this step's product.
+// Bound by latency for few tokens (128 x 4096 x 4096 MXFP4 5.6 us, the weights' bytes
+// take 1.3) and by the L2s beyond: every tile reads both its operands whole.
 #include "linear_common.h"
 
 namespace moe {
@@ -98,26 +100,28 @@ __global__ void __launch_bounds__(64 * kSplitWaves) linear_split_kernel(LinearAr
 template <bool F8, int NT, int NR>
 hipError_t launch_split(const LinearArgs& a, hipStream_t stream) {
   const int64_t rt = (a.N + NR * 16 - 1) / (NR * 16), tt = (a.T + NT * 16 - 1) / (NT * 16);
-  auto kern = linear_split_kernel<F8, NT, NR>;
-  const size_t lds = (size_t)kSplitWaves * NT * NR * 1024;
-  if (lds > 65536) {
-    const hipError_t err = raise_lds_limit(reinterpret_cast<const void*>(kern), lds);
-    if (err != hipSuccess) return err;
-  }
-  hipLaunchKernelGGL(kern, dim3((unsigned)((rt * tt + 7) / 8 * 8)), dim3(64 * kSplitWaves), lds, stream, a, (int)rt,
-                     (int)tt);
+  constexpr size_t lds = (size_t)kSplitWaves * NT * NR * 1024;
+  static_assert(lds <= 65536, "the default limit");
+  hipLaunchKernelGGL((linear_split_kernel<F8, NT, NR>), dim3((unsigned)((rt * tt + 7) / 8 * 8)),
+                     dim3(64 * kSplitWaves), lds, stream, a, (int)rt, (int)tt);
   return hipGetLastError();
+}
+
+// 16 rows a tile while those of 32 are fewer than the CUs, else 32 (us, K = 4096,
+// MXFP4, 16 / 32 / 64 rows: 64 x 4096 5.1 / 5.5 / 7.8, 128 x 4096 6.8 / 5.6 / 7.9, 256 x 4096 10.5
+// / 8.4 / 8.5, 64 x 16384 11.0 / 9.0 / 10.2; 32 x 4096 4.4 / 4.6, 32 x 16384 8.5 / 8.3; 16 tokens
+// with K = 16384: 1024 rows 8.3 / 8.8, 16384 rows 33.8 / 27.1).
+template <bool F8, int NT>
+hipError_t launch_split_rows(const LinearArgs& a, hipStream_t stream) {
+  const int64_t tiles32 = (int64_t)((a.N + 31) / 32) * ((a.T + NT * 16 - 1) / (NT * 16));
+  return tiles32 >= 256 ? launch_split<F8, NT, 2>(a, stream) : launch_split<F8, NT, 1>(a, stream);
 }
 
 template <bool F8>
 hipError_t launch_linear_type(const LinearArgs& a, hipStream_t stream) {
-  const int64_t b16 = (a.N + 15) / 16;
-  if (a.T <= 16) return b16 >= 512 ? launch_split<F8, 1, 2>(a, stream) : launch_split<F8, 1, 1>(a, stream);
-  if (a.T <= 32) return b16 >= 512 ? launch_split<F8, 2, 2>(a, stream) : launch_split<F8, 2, 1>(a, stream);
-  const int64_t t64 = (a.T + 63) / 64;
-  if (b16 / 4 * t64 >= 256) return launch_split<F8, 4, 4>(a, stream);
-  if (b16 / 2 * t64 >= 256) return launch_split<F8, 4, 2>(a, stream);
-  return launch_split<F8, 4, 1>(a, stream);
+  if (a.T <= 16) return launch_split_rows<F8, 1>(a, stream);
+  if (a.T <= 32) return launch_split_rows<F8, 2>(a, stream);
+  return launch_split_rows<F8, 4>(a, stream);
 }
 
 }  // namespace

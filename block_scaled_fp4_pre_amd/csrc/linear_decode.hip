@@ -9,6 +9,12 @@
 // takes w, w + 8, ...), each keeping its steps' token operands in registers, and
 // their sums meet in LDS, added in wave order.  The next block's weights are
 // loaded before this block's sums are exchanged.
+//
+// 1 x 4096 x 4096 MXFP4: 4.2 us, 2.1 TB/s with the launch in it (a token kernel and
+// the split kernel: 7.1); 1 x 4096 x 32000: 12.6 us, 5.5 TB/s; 16 x 2048 x 4096 E4M3
+// with addend 6.0.  Quantizing in the lanes that feed the MFMA, each wave its own
+// steps, took 5.8 us for one token: straight code for every step, fetched once
+// and run once, with one token's four lanes of a wave at work.
 #include "linear_common.h"
 #include "quant_e4m3.h"
 
@@ -164,6 +170,7 @@ __global__ void __launch_bounds__(kDecodeThreads) linear_decode_kernel(LinearArg
 template <bool F8, int SPW>
 hipError_t launch_decode(const LinearArgs& a, const LinearInput& in, hipStream_t stream) {
   const int blocks = (a.N + 15) / 16;
+  // at most two workgroups a CU: each keeps the tokens for all its blocks
   const int grid = (blocks < 512 ? blocks + 7 : 512) / 8 * 8;
   const size_t lds = (size_t)a.steps * ((F8 ? 2048 : 1024) + kWave);
   auto kern = linear_decode_kernel<F8, SPW>;

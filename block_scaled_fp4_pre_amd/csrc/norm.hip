@@ -13,7 +13,8 @@
 // The squares' sum, the reciprocal root and both products run in fp64 (full
 // rate on this chip, hidden behind the loads): the result is then rounded
 // the same way whatever the order of the sum, so the codes are reproducible
-// next to the quantizer's borders.
+// next to the quantizer's borders.  16384 x 4096 with residual and E4M3 codes (472
+// MB) take 92 us, 5.1 TB/s, the rate of a large copy; 1 x 4096 3.0 us, a launch.
 #include "launch_ops.h"
 #include "pack_bf16.h"
 #include "quant_e4m3.h"
@@ -245,6 +246,12 @@ hipError_t launch_norm(MOE_NORM_PARAMS) {
   return hipGetLastError();
 }
 
+// The smallest team that holds the row in at most 4 pieces a thread: a wave up to
+// 1024 values (no barrier), 4 waves up to 8192.  Measured with a bfloat16 residual,
+// y and E4M3 codes, us (wave / 4 waves / 16 waves): 65536 x 512 64 / 125 / 603,
+// 32768 x 1024 59 / 76 / 319, 16384 x 2048 66 / 59 / 178, 16384 x 4096 133 / 111 / 209, 8192 x
+// 8192 - / 121 / 129; one row of 2048 3.9 / 2.3 / 3.1, of 4096 6.4 / 2.9 / 3.3, of 8192 - /
+// 4.3 / 3.5.
 template <int RES, int ACT>
 hipError_t launch_norm_act(MOE_NORM_PARAMS) {
   if (cols <= 512) return launch_norm<RES, ACT, 64, 1>(MOE_NORM_ARGS);
