@@ -175,6 +175,8 @@ int check_norm_args(int32_t mma_type, int32_t res_dtype, int32_t w_dtype, int64_
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
       !aligned(y, 16) || !aligned(codes, 16))
     return MOE_EINVAL;
+  if (y != nullptr && (y == residual_out || y == codes)) return MOE_EINVAL;   // two outputs in one place
+  if (codes != nullptr && (codes == x || codes == residual || codes == residual_out)) return MOE_EINVAL;
   if (codes != nullptr) {
     if (mma_type != MOE_MMA_MXF4_X_MXF4 && mma_type != MOE_MMA_FP8_X_MXF4 && mma_type != MOE_MMA_NVF4_X_NVF4)
       return MOE_EUNSUPPORTED;
@@ -262,6 +264,9 @@ int check_linear_args(const moe_w4a4_linear_cfg* cfg, const void* prepared, int3
   if (!aligned(prepared, 256) || !aligned(workspace, 256) || !aligned(x, 16) || !aligned(xq, 16) ||
       !aligned(addend, 16) || !aligned(out, 16))
     return MOE_EINVAL;
+  // workgroups read x and xq while others write out; addend's element is read by
+  // the lane that writes it, which needs the two to have one type
+  if (out == x || out == xq || (out == addend && out_dtype == 1)) return MOE_EINVAL;
   if (workspace_bytes < linear_layout(cfg).workspace) return MOE_EWORKSPACE;
   return MOE_OK;
 }

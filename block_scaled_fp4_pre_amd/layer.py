@@ -153,7 +153,7 @@ class MoeW4A4Layer:
         one.  Returns (out, h): out = experts(y) (+ shared(y)) bf16 [T, H], and
         the new residual stream h = x + residual, of the residual's type.
         x bf16 [T, H]; residual bf16 / float32 [T, H] (residual_out like it,
-        may be it; a new tensor if None); norm_weight [H]; gate_weight [E, H]
+        may be it; a new tensor if None), or None (h is x then); norm_weight [H]; gate_weight [E, H]
         bf16 (logits by a plain product), or a W4A4Linear with out_features E;
         bias float32 [E]; shared: a W4A4Linear from H to H, added to the
         experts' output before its rounding.  Tokens past the fused
@@ -165,7 +165,7 @@ class MoeW4A4Layer:
         on_stream = torch.cuda.stream(torch.cuda.ExternalStream(int(stream), self.device)) if stream is not None \
             else contextlib.nullcontext()
         with torch.cuda.device(self.device), on_stream:
-            if residual_out is None:
+            if residual_out is None and residual is not None:
                 residual_out = torch.empty_like(residual)
             if out is None:
                 out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
@@ -192,7 +192,7 @@ class MoeW4A4Layer:
                                          _lib.MOE_STAGE_ALL & ~_lib.MOE_STAGE_QUANT)
             if shared is not None:
                 shared.forward(y, out=out, addend=out)
-        return out, residual_out
+        return out, x if residual is None else residual_out
 
     def run_stages(self, stages, num_tokens, x=None, topk_ids=None, topk_weights=None, out=None,
                    gemm1_acc=None, stream=None):

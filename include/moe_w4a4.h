@@ -296,7 +296,8 @@ int moe_w4a4_forward_noalloc(const moe_w4a4_cfg* cfg, const void* prepared, int3
  *   codes        NULL, or device uint8 [rows, cols/2] (E4M3: [rows, cols])
  *   scales       uint8 [rows, cols/32] (NVFP4: cols/16); NULL exactly when codes is
  * x, residual, weight, residual_out, y and codes 16-byte aligned; no other
- * overlap of inputs and outputs than the three named.  cols % 32 == 0, cols <=
+ * overlap of inputs and outputs than the three named (MOE_EINVAL where two
+ * outputs, or codes and an input, have one address).  cols % 32 == 0, cols <=
  * 65536, rows >= 0 (0 enqueues nothing and looks at no pointer), eps finite
  * and > 0; without codes mma_type and g are not looked at.  y or codes must be
  * given.  Values must be finite, and so must x + residual: a row with others
@@ -377,6 +378,7 @@ int moe_w4a4_linear_prepare(const moe_w4a4_linear_cfg* cfg, const uint8_t* codes
  * make them).  The result is the same, bit for bit.
  *   addend     NULL, or device bfloat16 [num_tokens, N], added to the fp32 sum
  *              before the one rounding; may be `out` itself when that is bfloat16
+ *              (out overlaps no other input: MOE_EINVAL where it is x or xq)
  *   out_dtype  0 = bfloat16, 1 = float32
  *   out        device [num_tokens, N] of out_dtype
  *   workspace  device buffer of query's workspace_bytes, 256-byte aligned: the

@@ -28,9 +28,9 @@ struct Norm {
   int32_t mma = MOE_MMA_FP8_X_MXF4, res = 0, w = 0;
   int64_t rows = 4;
   int32_t cols = 64;
-  const void *x = A, *residual = A, *weight = A;
+  const void *x = P(0x100000), *residual = P(0x200000), *weight = P(0x300000);
   float eps = 1e-6f, g = 1.0f;
-  const void *residual_out = A, *y = A, *codes = A, *scales = A;
+  const void *residual_out = P(0x400000), *y = P(0x500000), *codes = P(0x600000), *scales = P(0x700000);
   bool noop = false;
   int operator()() {
     return moe::check_norm_args(mma, res, w, rows, cols, x, residual, weight, eps, g, residual_out, y, codes, scales,
@@ -75,6 +75,12 @@ void norm() {
   NORM(a.y = P(0x100008), MOE_EINVAL);
   NORM(a.codes = P(0x100001), MOE_EINVAL);
   NORM(a.scales = P(0x100001), MOE_OK);
+  NORM(a.residual_out = a.residual; a.y = a.x, MOE_OK);      // in place
+  NORM(a.residual_out = a.x, MOE_OK);
+  NORM(a.y = a.residual_out, MOE_EINVAL);
+  NORM(a.codes = a.y, MOE_EINVAL);
+  NORM(a.codes = a.x, MOE_EINVAL);
+  NORM(a.codes = a.residual_out, MOE_EINVAL);
   NORM(a.rows = 0; a.x = a.weight = a.y = a.codes = nullptr, MOE_OK);
   Norm z;
   z.rows = 0;
@@ -142,7 +148,7 @@ struct Linear {
   int32_t tokens = 70;
   const void *x = A, *xq = nullptr, *xsf = nullptr, *addend = nullptr;
   int32_t dtype = 0;
-  const void *out = A, *workspace = A;
+  const void *out = P(0x800000), *workspace = A;
   size_t bytes = (size_t)1 << 30;
   bool noop = false;
   int operator()() {
@@ -218,6 +224,11 @@ void linear() {
   LINEAR(a.bytes = (size_t)moe::linear_layout(&a.c).workspace, MOE_OK);
   LINEAR(a.bytes = (size_t)moe::linear_layout(&a.c).workspace - 1, MOE_EWORKSPACE);
   LINEAR(a.c.mma_type = MOE_MMA_NVF4_X_NVF4, MOE_EUNSUPPORTED);
+  const void* const B = P(uintptr_t(1) << 21);             // overlaps
+  LINEAR(a.x = B; a.out = B, MOE_EINVAL);
+  LINEAR(a.x = nullptr; a.xq = B; a.xsf = A; a.out = B, MOE_EINVAL);
+  LINEAR(a.addend = B; a.out = B, MOE_OK);
+  LINEAR(a.addend = B; a.out = B; a.dtype = 1, MOE_EINVAL);
 }
 
 }  // namespace

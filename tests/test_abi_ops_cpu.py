@@ -35,14 +35,15 @@ def test_every_check_under_asan_and_ubsan(tmp_path):
 
 def test_entry_points_run_the_checks_before_any_hip_call():
     L = _lib.lib()
+    far = [ctypes.c_void_p((2 + i) << 20) for i in range(3)]
     norm = lambda rows, cols=64, x=FAKE: L.moe_w4a4_add_rmsnorm(1, 0, 0, rows, cols, x, None, FAKE, 1e-6, 1.0, None,  # noqa: E731
-                                                                 FAKE, FAKE, FAKE, None)
+                                                                 far[0], far[1], far[2], None)
     assert norm(4, 40) == _lib.MOE_EUNSUPPORTED and norm(4, 64, None) == _lib.MOE_EINVAL and norm(0) == _lib.MOE_OK
     router = lambda T, E=64: L.moe_w4a4_router(1, 0, T, E, 6, 1, 1, FAKE, None, 1, 1.0, FAKE, FAKE, None)  # noqa: E731
     assert router(4, 600) == _lib.MOE_EUNSUPPORTED and router(-1) == _lib.MOE_EINVAL and router(0) == _lib.MOE_OK
     cfg = _lib.make_linear_cfg(64, 32, 8)
     pb, wb = _lib.moe_w4a4_linear_query(cfg)
-    lin = lambda T, ws=wb: L.moe_w4a4_linear(ctypes.byref(cfg), FAKE, T, FAKE, None, None, None, 0, FAKE, FAKE, ws, None)  # noqa: E731
+    lin = lambda T, ws=wb: L.moe_w4a4_linear(ctypes.byref(cfg), FAKE, T, FAKE, None, None, None, 0, far[0], FAKE, ws, None)  # noqa: E731
     assert lin(9) == _lib.MOE_ECAPACITY and lin(4, wb - 1) == _lib.MOE_EWORKSPACE and lin(0, 0) == _lib.MOE_OK
     assert L.moe_w4a4_linear_prepare(ctypes.byref(cfg), FAKE, FAKE, FAKE, pb - 1, None) == _lib.MOE_EWORKSPACE
     if not torch.cuda.is_available():

@@ -268,3 +268,22 @@ def test_first_call_of_a_kernel_inside_a_capture(mma):
         torch.cuda.synchronize()
         got = out.clone()
         assert torch.equal(got, lin.forward(x))
+
+
+@TYPES
+@pytest.mark.parametrize("T", [3, 40, 1100])
+def test_subnormal_outputs(T, mma):
+    """Sums below 2^-126: the bfloat16 result is on its subnormal grid (2^-133 apart)."""
+    log(f"[test] linear subnormal outputs T {T} mma {mma}")
+    K, N = 64, 2050
+    v = bf16.decode(tokens(T, K, 36)) * 2.0 ** -60
+    x = bf16.encode(v)
+    wc, ws = weights(N, K, 37)
+    ws = (ws.astype(np.int32) - 63).astype(np.uint8)
+    lin = make_linear(K, N, T, mma, wc, ws)
+    _, _, ref, mag = reference(x, wc, ws, mma)
+    assert np.mean(np.abs(ref) < 2.0 ** -126) > 0.4                   # (of the case: enough of them are subnormal)
+    got = run(lin, x, T, N).double().cpu().numpy()
+    tol = linear.sum_error(mag, K, mma == FP8) + 2.0 ** -149          # fp32 sums may be subnormal too
+    assert np.all(np.abs(got - ref) <= tol + np.maximum(np.abs(ref) * 2.0 ** -8, 2.0 ** -134) * (1 + 2.0 ** -8))
+    assert np.count_nonzero(got) > got.size / 2

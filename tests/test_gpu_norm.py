@@ -200,3 +200,29 @@ def test_captured_and_replayed(cols):
         call()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (y, ro, c, s)))
+
+
+def test_subnormal_sums_and_outputs():
+    """bfloat16 results below 2^-126, in the residual and in y."""
+    log("[test] norm subnormal results")
+    rng = np.random.default_rng(20)
+    x = bf16.encode(np.ldexp(rng.integers(-127, 128, size=(4, 128)).astype(np.float64), -133))
+    r = np.ldexp(rng.integers(-127, 128, size=(4, 128)).astype(np.float64), -133)
+    check(x, r, "bf16", np.ones(128), False, FP8)
+    check(make(4, 128, 21), None, None, np.full(128, 2.0 ** -130), False, MX4)
+    check(make(4, 128, 22), None, None, 2.0 ** -np.linspace(100, 148, 128).round(), False, None)
+
+
+def test_more_rows_than_blocks():
+    """Over 2^20 rows a workgroup takes several; the same rows give the same bits."""
+    log("[test] norm with more rows than workgroups")
+    rows, cols, part = (1 << 20) + 70_001, 1056, 1000
+    x = dev_bf16(make(part, cols, 23)).repeat(-(-rows // part), 1)[:rows].contiguous()
+    y = torch.empty_like(x)
+    _lib.moe_w4a4_add_rmsnorm(x, None, torch.ones(cols, device="cuda"), EPS, y=y)
+    few = torch.empty((part, cols), dtype=torch.bfloat16, device="cuda")
+    _lib.moe_w4a4_add_rmsnorm(x[:part].contiguous(), None, torch.ones(cols, device="cuda"), EPS, y=few)
+    torch.cuda.synchronize()
+    whole = rows // part * part
+    assert torch.equal(y[:whole].view(-1, part, cols).amin(0), few) and torch.equal(y[:whole].view(-1, part, cols).amax(0), few)
+    assert torch.equal(y[whole:], few[:rows - whole])
