@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(
         for (int i = 1; i < EPL; ++i)
           if (key[i] > best) {
             best = key[i];
-            val = l[i];
+            if constexpr (BIAS) val = l[i];
             at = i * kWave + lane;
           }
         const uint32_t m = wave_max(best);
@@ -262,7 +262,9 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(
             owner = o;
           }
         }
-        const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(val), owner));
+        // (without a bias the key is the logit)
+        const float v = BIAS ? __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(val), owner))
+                             : key_value(m);
         if (j < k && lane == j) {
           mine = e;
           logit = v;
