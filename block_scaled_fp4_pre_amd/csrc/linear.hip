@@ -85,7 +85,6 @@ __global__ void __launch_bounds__(64 * kSplitWaves) linear_split_kernel(LinearAr
 #pragma unroll
     for (int r = 0; r < NR; ++r) red[((wave * NT + c) * NR + r) * kWave + lane] = acc[c][r];
   __syncthreads();
-  const bool whole = p.N % 4 == 0;
   for (int i = threadIdx.x; i < NT * 16 * NR * 4; i += 64 * kSplitWaves) {
     const int t = i / (NR * 4), q = i - t * (NR * 4);
     const int at = ((t / 16) * NR + q / 4) * kWave + (q % 4) * 16 + t % 16;
@@ -93,7 +92,7 @@ __global__ void __launch_bounds__(64 * kSplitWaves) linear_split_kernel(LinearAr
 #pragma unroll
     for (int w = 1; w < kSplitWaves; ++w) v += red[w * NT * NR * kWave + at];
     const int tok = tt * NT * 16 + t, n = rt * NR * 16 + 4 * q;
-    if (tok < p.T && n < p.N) store4(p, tok, n, v, whole);
+    if (tok < p.T && n < p.N) store4(p, tok, n, v);
   }
 }
 

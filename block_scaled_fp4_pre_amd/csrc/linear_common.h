@@ -29,18 +29,25 @@ __device__ __forceinline__ size_t unit_base(int u, int steps) {
   return ((size_t)(u / kGroupUnits) * steps * kGroupUnits + u % kGroupUnits) * CB;
 }
 
-// out[t, n..n+3] = v (+ addend), n a multiple of 4; `whole`: N % 4 == 0, so
-// that the four are in one row and aligned.
-__device__ __forceinline__ void store4(const LinearArgs& a, int t, int n, v4f v, bool whole) {
+// Vectors at the alignment of one value of `out` (or the addend): rows of any N
+// are read and written in whole vectors, which the memory unit takes at any address.
+// (One value at a time where N does not keep rows aligned: 11342 x 64 x 14298
+// MXFP4 244 against 137 us, 8847 x 64 x 7586 with an addend 208 against 95.)
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef v2u v2u_at2 __attribute__((aligned(2)));
+typedef v4u v4u_at2 __attribute__((aligned(2)));
+typedef v4f v4f_at4 __attribute__((aligned(4)));
+
+// out[t, n..n+3] = v (+ addend), as far as the row goes.
+__device__ __forceinline__ void store4(const LinearArgs& a, int t, int n, v4f v) {
   const size_t i = (size_t)t * a.N + n;
   const int left = a.N - n;
+  const bool whole = left >= 4;
   if (a.addend != nullptr) {
     if (whole) {
-      const uint2 r = *reinterpret_cast<const uint2*>(a.addend + i);
-      v[0] += bf16_to_f32(r.x & 0xFFFFu);
-      v[1] += bf16_to_f32(r.x >> 16);
-      v[2] += bf16_to_f32(r.y & 0xFFFFu);
-      v[3] += bf16_to_f32(r.y >> 16);
+      const v2u r = *reinterpret_cast<const v2u_at2*>(a.addend + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += bf16_to_f32(r[j / 2] >> (j % 2 * 16) & 0xFFFFu);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -50,7 +57,7 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int t, int n, v4f v,
   if (a.out_f32) {
     float* o = static_cast<float*>(a.out) + i;
     if (whole) {
-      *reinterpret_cast<v4f*>(o) = v;
+      *reinterpret_cast<v4f_at4*>(o) = v;
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -59,7 +66,7 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int t, int n, v4f v,
   } else {
     uint16_t* o = static_cast<uint16_t*>(a.out) + i;
     if (whole) {
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      *reinterpret_cast<v2u_at2*>(o) = v2u{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)

@@ -138,7 +138,6 @@ __global__ void __launch_bounds__(kDecodeThreads) linear_decode_kernel(LinearArg
       sb[i] = scales[s * kWave + lane];
     }
   }
-  const bool whole = p.N % 4 == 0;
   int flip = 0;
   for (int blk = first; blk < blocks; blk += gridDim.x) {
     v4f acc = {0.f, 0.f, 0.f, 0.f};
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(kDecodeThreads) linear_decode_kernel(LinearArg
 #pragma unroll
       for (int w = 1; w < kDecodeWaves; ++w) v += red[flip][w][lane];
       const int t = lane & 15, n = blk * 16 + 4 * kb;
-      if (t < p.T && n < p.N) store4(p, t, n, v, whole);
+      if (t < p.T && n < p.N) store4(p, t, n, v);
     }
     flip ^= 1;
   }

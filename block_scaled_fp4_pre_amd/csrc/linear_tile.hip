@@ -94,7 +94,7 @@ __device__ __forceinline__ void tile_store(const LinearArgs& p, const uint8_t* m
   static_assert(G * 16 % (IT * TPP) == 0, "whole passes");
   const int n = n0 + lane % LPT * V, tl = lane / LPT;
   const int left = max(0, min(V, p.N - n));
-  const bool whole = p.N % V == 0;                         // then V or none are left, and aligned
+  const bool whole = left == V;
   const int live = left > 0 ? live_tokens : 0;
 #pragma unroll 1
   for (int i0 = tl; i0 < G * 16; i0 += IT * TPP) {
@@ -111,11 +111,11 @@ __device__ __forceinline__ void tile_store(const LinearArgs& p, const uint8_t* m
             for (int j = 0; j < V; ++j)
               if (j < left) add[i][j / 2] |= (uint32_t)a[j] << (j % 2 * 16);
           } else if constexpr (F32) {
-            const uint64_t q = __builtin_nontemporal_load(reinterpret_cast<const uint64_t*>(a));
-            add[i][0] = (uint32_t)q;
-            add[i][1] = (uint32_t)(q >> 32);
+            const v2u q = __builtin_nontemporal_load(reinterpret_cast<const v2u_at2*>(a));
+            add[i][0] = q[0];
+            add[i][1] = q[1];
           } else {
-            add[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(a));
+            add[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u_at2*>(a));
           }
         }
       }
@@ -138,7 +138,7 @@ __device__ __forceinline__ void tile_store(const LinearArgs& p, const uint8_t* m
       if constexpr (F32) {
         float* o = static_cast<float*>(p.out) + at + (size_t)(i * TPP) * p.N;
         if (whole) {
-          __builtin_nontemporal_store(v[i][0], reinterpret_cast<v4f*>(o));
+          __builtin_nontemporal_store(v[i][0], reinterpret_cast<v4f_at4*>(o));
         } else {
 #pragma unroll
           for (int j = 0; j < V; ++j)
@@ -150,7 +150,7 @@ __device__ __forceinline__ void tile_store(const LinearArgs& p, const uint8_t* m
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[j] = pack_bf16(v[i][j / 2][j % 2 * 2], v[i][j / 2][j % 2 * 2 + 1]);
         if (whole) {
-          __builtin_nontemporal_store(h, reinterpret_cast<v4u*>(o));
+          __builtin_nontemporal_store(h, reinterpret_cast<v4u_at2*>(o));
         } else {
 #pragma unroll
           for (int j = 0; j < V; ++j)

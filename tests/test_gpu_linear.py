@@ -287,3 +287,23 @@ def test_subnormal_outputs(T, mma):
     tol = linear.sum_error(mag, K, mma == FP8) + 2.0 ** -149          # fp32 sums may be subnormal too
     assert np.all(np.abs(got - ref) <= tol + np.maximum(np.abs(ref) * 2.0 ** -8, 2.0 ** -134) * (1 + 2.0 ** -8))
     assert np.count_nonzero(got) > got.size / 2
+
+
+@TYPES
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,N0", [(5, 264), (90, 264), (1100, 1000), (2100, 1096), (8192, 2032)])
+def test_rows_of_any_length(T, N0, dtype, mma):
+    """Rows at every remainder of eight values, through each kernel, with an
+    addend: the columns' bits are those of rows that are aligned, and the rows'
+    own last values are the last ones written."""
+    log(f"[test] linear rows T {T} N {N0} {dtype} mma {mma}")
+    K = 96
+    x, (wc, ws), add = tokens(T, K, 31), weights(N0 + 8, K, 32), tokens(T, N0 + 8, 33)
+    lin = make_linear(K, N0 + 8, T, mma, wc, ws)
+    _, _, ref, mag = reference(x, wc, ws, mma, bf16.decode(add))
+    whole = run(lin, x, T, N0 + 8, dtype=dtype, addend=dev_bf16(add)).clone()
+    close(whole.double().cpu().numpy(), ref, mag + np.abs(bf16.decode(add)), K, mma, f32=dtype == torch.float32)
+    for N in range(N0 + 1, N0 + 8):
+        lin = make_linear(K, N, T, mma, np.ascontiguousarray(wc[:N]), np.ascontiguousarray(ws[:N]))
+        got = run(lin, x, T, N, dtype=dtype, addend=dev_bf16(np.ascontiguousarray(add[:, :N])))
+        assert torch.equal(got, whole[:, :N]), N
