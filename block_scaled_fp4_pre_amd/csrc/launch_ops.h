@@ -57,12 +57,27 @@ struct LinearInput {
 // waves share the K steps, up to 128 tiles of 128 rows x 64 tokens (half the CUs);
 // those with two groups of waves up to one a CU; tiles of 128 x 128, two a CU; and
 // of 256 rows x 128 tokens once these give every CU its two.
-// Up to kDecodeMaxTokens tokens and kDecodeMaxSteps K steps: the decode kernel,
-// which needs no tokens in tile order.
-constexpr int kDecodeMaxTokens = 16, kDecodeMaxSteps = 64;
+// Few tokens: the decode kernel, which needs no tokens in tile order and so no
+// launch before it, but quantizes them in every workgroup.  Passes of one call, us,
+// decode against the token kernel and split, MXFP4 (E4M3 within 2 us of these):
+//   tokens x K     N 4096        N 8192        N 16384       N 32000
+//   1 x 4096       5.8 / 8.9     5.9 / 9.3     7.6 / 9.8     12.2 / 15.5
+//   8 x 4096       5.5 / 8.8     7.9 / 9.0     10.3 / 9.9    13.2 / 15.2
+//   16 x 2048      6.3 / 9.2     6.9 / 8.8     8.4 / 9.2     10.0 / 11.0
+//   16 x 4096      6.9 / 9.0     11.1 / 9.4    12.9 / 10.0   16.1 / 15.6
+//   1 x 8192       8.6 / 8.8     -             15.7 / 14.2   -              (N 2048: 6.8 / 8.9)
+//   4 x 8192       9.9 / 9.0     -             17.1 / 14.3   -
+// So where tokens times K steps are kDecodeMaxWork at most, or there is one block
+// of 16 rows a CU; past 32 steps, where a wave holds 8 of them, for one token.
+constexpr int kDecodeMaxTokens = 16, kDecodeMaxSteps = 64, kDecodeMaxWork = 256;
 enum LinearPlan { kLinearDecode, kLinearSplit, kLinearTile64, kLinearTile128, kLinearTile256 };
+inline bool linear_decodes(int T, int N, int steps) {
+  const bool a_block_a_cu = N <= 256 * 16;
+  if (steps > kDecodeMaxSteps / 2) return T == 1 && steps <= kDecodeMaxSteps && a_block_a_cu;
+  return T <= kDecodeMaxTokens && (T * steps <= kDecodeMaxWork || a_block_a_cu);
+}
 inline LinearPlan linear_plan(int T, int N, int steps) {
-  if (T <= kDecodeMaxTokens && steps <= kDecodeMaxSteps) return kLinearDecode;
+  if (linear_decodes(T, N, steps)) return kLinearDecode;
   const int64_t t64 = (T + 63) / 64, t128 = (T + 127) / 128, n128 = (N + 127) / 128, n256 = (N + 255) / 256;
   if (t64 * n128 <= 128) return kLinearSplit;
   if (t64 * n128 <= 256) return kLinearTile64;

@@ -169,11 +169,14 @@ __global__ void __launch_bounds__(kDecodeThreads) linear_decode_kernel(LinearArg
 template <bool F8, int SPW>
 hipError_t launch_decode(const LinearArgs& a, const LinearInput& in, hipStream_t stream) {
   const int blocks = (a.N + 15) / 16;
-  // at most two workgroups a CU: each keeps the tokens for all its blocks
-  const int grid = (blocks < 512 ? blocks + 7 : 512) / 8 * 8;
-  const size_t lds = (size_t)a.steps * ((F8 ? 2048 : 1024) + kWave);
+  const size_t lds = (size_t)a.steps * ((F8 ? 2048 : 1024) + kWave), all = lds + sizeof(v4f) * 2 * kDecodeThreads;
+  // No more workgroups than the CUs hold at a time, at most two each: each
+  // quantizes the tokens for all its blocks, and one that has to wait for another's
+  // LDS would do so after it.
+  const int most = 2 * all <= 160 * 1024 ? 512 : 256;
+  const int grid = (blocks < most ? blocks + 7 : most) / 8 * 8;
   auto kern = linear_decode_kernel<F8, SPW>;
-  if (lds + sizeof(v4f) * 2 * kDecodeThreads > 65536) {
+  if (all > 65536) {
     const hipError_t err = raise_lds_limit(reinterpret_cast<const void*>(kern), kDecodeMaxSteps * (2048 + kWave));
     if (err != hipSuccess) return err;
   }

@@ -307,3 +307,23 @@ def test_rows_of_any_length(T, N0, dtype, mma):
         lin = make_linear(K, N, T, mma, np.ascontiguousarray(wc[:N]), np.ascontiguousarray(ws[:N]))
         got = run(lin, x, T, N, dtype=dtype, addend=dev_bf16(np.ascontiguousarray(add[:, :N])))
         assert torch.equal(got, whole[:, :N]), N
+
+
+# on either side of what launch_ops.h's linear_plan sends to the decode kernel
+FEW = [(1, 8192, 100), (1, 8160, 33), (1, 4128, 4096), (1, 4128, 4097), (1, 8224, 64), (2, 4128, 64), (1, 4096, 8200),
+       (8, 4096, 5000), (9, 4096, 4100), (16, 2048, 4100), (16, 4096, 4096), (16, 4064, 4112), (16, 2080, 16)]
+
+
+@TYPES
+@pytest.mark.parametrize("T,K,N", FEW)
+def test_few_tokens(T, K, N, mma):
+    log(f"[test] linear few T {T} K {K} N {N} mma {mma}")
+    x, (wc, ws), add = tokens(T, K, 41), weights(N, K, 42), tokens(T, N, 43)
+    lin = make_linear(K, N, T, mma, wc, ws)
+    c, s, ref, mag = reference(x, wc, ws, mma)
+    got = run(lin, x, T, N)
+    close(got.double().cpu().numpy(), ref, mag, K, mma)
+    assert torch.equal(run(lin, x, T, N, quantized=(c, s)), got)
+    a = bf16.decode(add)
+    plus = run(lin, x, T, N, dtype=torch.float32, addend=dev_bf16(add))
+    close(plus.double().cpu().numpy(), ref + a, mag + np.abs(a), K, mma, f32=True)
