@@ -5,7 +5,7 @@
 //
 // Bound by HBM: every input is read once and every output written once; the row
 // stays in registers between the sum and the norm, so nothing is read twice.
-// A team of 64, 256 or 1024 threads owns a row; a thread holds CPL pieces of
+// A team of 64 to 1024 threads owns a row; a thread holds CPL pieces of
 // 8 consecutive values (16-byte loads), so four neighbouring lanes share an
 // MX group of 32 (two an NVFP4 block of 16) and exchange its absolute maximum
 // by two (one) DPP steps inside their quad.
@@ -251,7 +251,10 @@ hipError_t launch_norm(MOE_NORM_PARAMS) {
 // y and E4M3 codes, us (wave / 4 waves / 16 waves): 65536 x 512 64 / 125 / 603,
 // 32768 x 1024 59 / 76 / 319, 16384 x 2048 66 / 59 / 178, 16384 x 4096 133 / 111 / 209, 8192 x
 // 8192 - / 121 / 129; one row of 2048 3.9 / 2.3 / 3.1, of 4096 6.4 / 2.9 / 3.3, of 8192 - /
-// 4.3 / 3.5.
+// 4.3 / 3.5.  Past 8192 values 8 waves of 4 pieces where there are more rows than CUs:
+// more rows are in flight (no residual / bfloat16 / float32 one, y and E4M3 codes, 8
+// against 16 waves: 6798 x 9504 100 / 120 / 172 against 110 / 131 / 170, 512 x 16384 11.8 / 12.5
+// / 20.1 against 12.6 / 14.3 / 22.0; 64 x 16384 5.6 / 6.2 / 6.9 against 5.1 / 5.8 / 6.9).
 template <int RES, int ACT>
 hipError_t launch_norm_act(MOE_NORM_PARAMS) {
   if (cols <= 512) return launch_norm<RES, ACT, 64, 1>(MOE_NORM_ARGS);
@@ -259,6 +262,7 @@ hipError_t launch_norm_act(MOE_NORM_PARAMS) {
   if (cols <= 2048) return launch_norm<RES, ACT, 256, 1>(MOE_NORM_ARGS);
   if (cols <= 4096) return launch_norm<RES, ACT, 256, 2>(MOE_NORM_ARGS);
   if (cols <= 8192) return launch_norm<RES, ACT, 256, 4>(MOE_NORM_ARGS);
+  if (cols <= 16384 && rows > 256) return launch_norm<RES, ACT, 512, 4>(MOE_NORM_ARGS);
   if (cols <= 16384) return launch_norm<RES, ACT, 1024, 2>(MOE_NORM_ARGS);
   if (cols <= 32768) return launch_norm<RES, ACT, 1024, 4>(MOE_NORM_ARGS);
   return launch_norm<RES, ACT, 1024, 8>(MOE_NORM_ARGS);

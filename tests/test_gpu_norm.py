@@ -226,3 +226,13 @@ def test_more_rows_than_blocks():
     whole = rows // part * part
     assert torch.equal(y[:whole].view(-1, part, cols).amin(0), few) and torch.equal(y[:whole].view(-1, part, cols).amax(0), few)
     assert torch.equal(y[whole:], few[:rows - whole])
+
+
+# past 8192 values the row count chooses the team: both sides of the change
+@pytest.mark.parametrize("rows", [256, 257, 300])
+@pytest.mark.parametrize("cols,res,mma", [(8224, None, FP8), (9504, "bf16", MX4), (16384, "f32", NV4), (16352, None, None)])
+def test_many_long_rows(rows, cols, res, mma):
+    log(f"[test] norm long rows {rows} x {cols} residual {res} format {mma}")
+    rng = np.random.default_rng(rows + cols)
+    r = None if res is None else rng.normal(size=(rows, cols))
+    check(make(rows, cols, cols), r, res, np.exp(0.3 * rng.normal(size=cols)), False, mma, inplace=rows == 300)
