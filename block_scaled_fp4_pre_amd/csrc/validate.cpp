@@ -175,8 +175,14 @@ int check_norm_args(int32_t mma_type, int32_t res_dtype, int32_t w_dtype, int64_
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
       !aligned(y, 16) || !aligned(codes, 16))
     return MOE_EINVAL;
-  if (y != nullptr && (y == residual_out || y == codes)) return MOE_EINVAL;   // two outputs in one place
-  if (codes != nullptr && (codes == x || codes == residual || codes == residual_out)) return MOE_EINVAL;
+  // An output in the place of another, or of an input whose rows it does not
+  // cover value for value (other workgroups may not have read those yet).
+  if (y != nullptr && (y == residual_out || y == weight || (y == residual && res_dtype == 1))) return MOE_EINVAL;
+  if (residual_out != nullptr && (residual_out == weight || (residual_out == x && res_dtype == 1))) return MOE_EINVAL;
+  auto taken = [&](const void* p) {
+    return p != nullptr && (p == x || p == residual || p == weight || p == residual_out || p == y);
+  };
+  if (taken(codes) || taken(scales) || (codes != nullptr && codes == scales)) return MOE_EINVAL;
   if (codes != nullptr) {
     if (mma_type != MOE_MMA_MXF4_X_MXF4 && mma_type != MOE_MMA_FP8_X_MXF4 && mma_type != MOE_MMA_NVF4_X_NVF4)
       return MOE_EUNSUPPORTED;

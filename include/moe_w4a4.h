@@ -292,15 +292,16 @@ int moe_w4a4_forward_noalloc(const moe_w4a4_cfg* cfg, const void* prepared, int3
  *   weight       device [cols] of w_dtype (0 = bfloat16, 1 = float32)
  *   residual_out device [rows, cols] of res_dtype: h; NULL exactly when residual is.
  *                May be `residual` itself (or x, if that has its type)
- *   y            NULL, or device bfloat16 [rows, cols]; may be x itself
+ *   y            NULL, or device bfloat16 [rows, cols]; may be x itself, or
+ *                `residual` if that is bfloat16 and not residual_out
  *   codes        NULL, or device uint8 [rows, cols/2] (E4M3: [rows, cols])
  *   scales       uint8 [rows, cols/32] (NVFP4: cols/16); NULL exactly when codes is
  * x, residual, weight, residual_out, y and codes 16-byte aligned; no other
- * overlap of inputs and outputs than the three named (MOE_EINVAL where two
- * outputs, or codes and an input, have one address).  cols % 32 == 0, cols <=
- * 65536, rows >= 0 (0 enqueues nothing and looks at no pointer), eps finite
- * and > 0; without codes mma_type and g are not looked at.  y or codes must be
- * given.  Values must be finite, and so must x + residual: a row with others
+ * overlap of inputs and outputs than those named (MOE_EINVAL where an output
+ * has the address of another, or of an input that it may not be).
+ * cols % 32 == 0, cols <= 65536, rows >= 0 (0 enqueues nothing and looks at no
+ * pointer), eps finite and > 0; without codes mma_type and g are not looked
+ * at.  y or codes must be given.  Values must be finite, and so must x + residual: a row with others
  * gets a y with NaN or infinity in it and unspecified codes; other rows are
  * untouched by it.  xq and xsf of the forward's workspace may be the codes and
  * scales here: moe_w4a4_run_stages without MOE_STAGE_QUANT then starts from

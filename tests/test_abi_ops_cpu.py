@@ -116,3 +116,16 @@ def test_binding_refuses_another_device(current_device_0, monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     with pytest.raises(ValueError, match="current device"):
         _lib.moe_w4a4_router(_t((4, 64), F32), _t((4, 6), I32), _t((4, 6), F32))
+
+
+def test_buffers_that_share_an_address(tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("g++ not available")
+    exe = tmp_path / "ops_overlap_check"
+    cmd = [gxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+           os.path.join(CSRC, "validate.cpp"), os.path.join(HERE, "ops_overlap_check.cpp"), "-o", str(exe)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip().endswith(" 0 failed"), r.stdout + r.stderr
