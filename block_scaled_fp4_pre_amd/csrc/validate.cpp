@@ -270,9 +270,11 @@ int check_linear_args(const moe_w4a4_linear_cfg* cfg, const void* prepared, int3
   if (!aligned(prepared, 256) || !aligned(workspace, 256) || !aligned(x, 16) || !aligned(xq, 16) ||
       !aligned(addend, 16) || !aligned(out, 16))
     return MOE_EINVAL;
-  // workgroups read x and xq while others write out; addend's element is read by
-  // the lane that writes it, which needs the two to have one type
-  if (out == x || out == xq || (out == addend && out_dtype == 1)) return MOE_EINVAL;
+  // workgroups read the tokens, the weights and the workspace while others write
+  // out; addend's element is read by the lane that writes it, which needs the two
+  // to have one type
+  if (out == x || out == xq || out == xsf || out == prepared || out == workspace || (out == addend && out_dtype == 1))
+    return MOE_EINVAL;
   if (workspace_bytes < linear_layout(cfg).workspace) return MOE_EWORKSPACE;
   return MOE_OK;
 }

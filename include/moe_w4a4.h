@@ -379,7 +379,8 @@ int moe_w4a4_linear_prepare(const moe_w4a4_linear_cfg* cfg, const uint8_t* codes
  * make them).  The result is the same, bit for bit.
  *   addend     NULL, or device bfloat16 [num_tokens, N], added to the fp32 sum
  *              before the one rounding; may be `out` itself when that is bfloat16
- *              (out overlaps no other input: MOE_EINVAL where it is x or xq)
+ *              (out overlaps nothing else: MOE_EINVAL where it has the address of
+ *              x, xq, xsf, prepared or workspace)
  *   out_dtype  0 = bfloat16, 1 = float32
  *   out        device [num_tokens, N] of out_dtype
  *   workspace  device buffer of query's workspace_bytes, 256-byte aligned: the

@@ -61,10 +61,34 @@ void norm() {
   NORM(a.y = nullptr; a.residual = a.residual_out = nullptr, MOE_OK);
 }
 
+struct Linear {
+  moe_w4a4_linear_cfg c{96, 100, 70, MOE_MMA_MXF4_X_MXF4};
+  const void *prepared = P(0x1000000), *x = nullptr, *xq = P(0x2000000), *xsf = P(0x3000000), *addend = nullptr,
+             *out = P(0x5000000), *workspace = P(0x6000000);
+  int operator()() {
+    bool noop = false;
+    return moe::check_linear_args(&c, prepared, 70, x, xq, xsf, addend, 0, out, workspace, (size_t)1 << 30, &noop);
+  }
+};
+#define LINEAR(set, want) do { Linear a; set; expect(a(), want, "linear: " #set); } while (0)
+
+void linear() {
+  LINEAR(, MOE_OK);
+  LINEAR(a.out = a.xq, MOE_EINVAL);
+  LINEAR(a.out = a.xsf, MOE_EINVAL);
+  LINEAR(a.out = a.prepared, MOE_EINVAL);
+  LINEAR(a.out = a.workspace, MOE_EINVAL);
+  LINEAR(a.x = a.out; a.xq = a.xsf = nullptr, MOE_EINVAL);
+  LINEAR(a.addend = a.out, MOE_OK);
+}
+
 }  // namespace
 
-int main() {
-  norm();
+int main(int argc, char** argv) {
+  if (argc > 1 && argv[1][0] == 'l')
+    linear();
+  else
+    norm();
   printf("%d cases, %d failed\n", g_cases, g_fail);
   return g_fail != 0;
 }

@@ -118,7 +118,8 @@ def test_binding_refuses_another_device(current_device_0, monkeypatch):
         _lib.moe_w4a4_router(_t((4, 64), F32), _t((4, 6), I32), _t((4, 6), F32))
 
 
-def test_buffers_that_share_an_address(tmp_path):
+@pytest.mark.parametrize("operator", ["norm", "linear"])
+def test_buffers_that_share_an_address(operator, tmp_path):
     gxx = shutil.which("g++")
     if gxx is None:
         pytest.skip("g++ not available")
@@ -127,5 +128,5 @@ def test_buffers_that_share_an_address(tmp_path):
            os.path.join(CSRC, "validate.cpp"), os.path.join(HERE, "ops_overlap_check.cpp"), "-o", str(exe)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
-    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    r = subprocess.run([str(exe), operator], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip().endswith(" 0 failed"), r.stdout + r.stderr
