@@ -444,12 +444,13 @@ def moe_w4a4_linear(cfg: moe_w4a4_linear_cfg, prepared, x, out, workspace, xq=No
     pw = _fits(prepared, "prepared", _U8, prepared.shape, dev)
     pk = _fits(workspace, "workspace", _U8, workspace.shape, dev)
     _linear_call(ctypes.byref(cfg), cfg.in_features, cfg.out_features, cfg.mma_type, dev, pw, x, out, pk,
-                 workspace.numel(), xq, xsf, addend, stream)
+                 workspace.numel(), xq, xsf, addend, stream, prepared.numel())
 
 
 def _linear_call(cfg_ref, K: int, N: int, mma_type: int, dev: int, prepared: int, x, out, workspace: int,
-                 workspace_bytes: int, xq, xsf, addend, stream) -> None:
-    """moe_w4a4_linear with the caller's own buffers as addresses (layer.W4A4Linear)."""
+                 workspace_bytes: int, xq, xsf, addend, stream, prepared_bytes: int | None = None) -> None:
+    """moe_w4a4_linear with the caller's own buffers as addresses
+    (layer.W4A4Linear, which made its weights' buffer: prepared_bytes None)."""
     px = pq = ps = pa = None
     if x is not None:
         if xq is not None or xsf is not None:
@@ -465,6 +466,11 @@ def _linear_call(cfg_ref, K: int, N: int, mma_type: int, dev: int, prepared: int
     if addend is not None:
         pa = _fits(addend, "addend", _BF16, (T, N), dev)
     po = _fits(out, "out", _BF16_F32, (T, N), dev)
+    if prepared_bytes is not None:
+        need = _sz()
+        _check(_lib.moe_w4a4_linear_query(cfg_ref, ctypes.byref(need), None), "moe_w4a4_linear_query")
+        if prepared_bytes < need.value:
+            raise ValueError(f"prepared: {prepared_bytes} bytes, at least {need.value} needed")
     st = _lib.moe_w4a4_linear(cfg_ref, prepared, T, px, pq, ps, pa, 1 if out.dtype is torch.float32 else 0, po,
                               workspace, workspace_bytes, _raw_stream(stream, dev))
     if st != MOE_OK:

@@ -230,8 +230,9 @@ class W4A4Linear:
         pb, wb = _lib.moe_w4a4_linear_query(self.cfg)
         if prepared is None:
             prepared = torch.empty(pb, dtype=torch.uint8, device=self.device)
-        elif prepared.numel() < pb or prepared.device != self.device:
-            raise ValueError("shared prepared buffer is too small or on another device")
+        elif (not prepared.is_contiguous() or prepared.numel() * prepared.element_size() < pb
+              or prepared.device != self.device):
+            raise ValueError("shared prepared buffer is too small, not contiguous or on another device")
         self.prepared = prepared
         self.workspace = torch.empty(max(wb, 1), dtype=torch.uint8, device=self.device)
         self._cfg_ref, self._workspace_bytes = ctypes.byref(self.cfg), wb

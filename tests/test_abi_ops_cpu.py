@@ -130,3 +130,28 @@ def test_buffers_that_share_an_address(operator, tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([str(exe), operator], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip().endswith(" 0 failed"), r.stdout + r.stderr
+
+
+def test_binding_refuses_weights_that_are_too_short(monkeypatch):
+    """The product reads all of the prepared weights, and is told only where they begin."""
+    def reached(*a):
+        raise AssertionError("the library was called")
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(_lib, "_raw_stream", lambda stream, dev: None)
+    monkeypatch.setattr(_lib._lib, "moe_w4a4_linear", reached)
+    cfg = _lib.make_linear_cfg(64, 32, 8)
+    pb, wb = _lib.moe_w4a4_linear_query(cfg)
+    call = lambda n: _lib.moe_w4a4_linear(cfg, _t((n,), U8), _t((4, 64)), _t((4, 32)), _t((wb,), U8))  # noqa: E731
+    with pytest.raises(ValueError, match="prepared"):
+        call(pb - 1)
+    with pytest.raises(AssertionError, match="library"):
+        call(pb)
+
+
+def test_linear_refuses_shared_weights_with_gaps():
+    """A strided view has enough elements, but not from its first address on."""
+    from block_scaled_fp4_pre_amd.layer import W4A4Linear
+    pb, _ = _lib.moe_w4a4_linear_query(_lib.make_linear_cfg(64, 32, 8))
+    for bad in (_t((2 * pb,), U8)[::2], _t((pb - 1,), U8), _t((1,), U8).expand(pb)):
+        with pytest.raises(ValueError, match="prepared"):
+            W4A4Linear(64, 32, 8, "cuda:0", prepared=bad)
