@@ -87,7 +87,13 @@ __device__ __forceinline__ void wave_lds_fence() {
 
 // Score of a logit that can be chosen; softmax before its division.
 __device__ __forceinline__ float score32(int scoring, float l, float top) {
-  if (scoring == MOE_SCORE_SOFTMAX) return expf(l - top);
+  if (scoring == MOE_SCORE_SOFTMAX) {
+    // exp(l - top) with the rounding of the difference put back: half a step of it
+    // is 2^-18 from 64 on, far more than the bits of the exponential.
+    const float d = l - top, t = d - l, r = (l - (d - t)) - (top + t);   // d + r == l - top
+    const float q = expf(d);
+    return q > 0.0f ? fmaf(q, r, q) : q;                                 // (d may be -infinity)
+  }
   const float e = expf(-fabsf(l));
   if (scoring == MOE_SCORE_SIGMOID) return (l < 0.0f ? e : 1.0f) / (1.0f + e);
   // far below zero log(1 + exp(l)) is exp(l) and would lose its bits there
@@ -158,12 +164,16 @@ __global__ void __launch_bounds__(kRouterThreads) router_kernel(
 #pragma unroll
         for (int i = 0; i < EPL; ++i) key[i] = order_key(l[i]);
       } else if (!exact) {
-        // By the library's documented bounds (exp 3, log1p 2, sqrt 3, division
-        // 2.5 last bits) a float32 score is within 7 last bits of the exact one, its
-        // sum with the bias half a bit more: below 2^-20 of the row's largest
-        // magnitude, 2^-19 for the two sides of a comparison.  A softmax's sum
-        // adds as much again.  (Scores below 2^-126: 2^-149 absolute.)
-        constexpr float kMargin = scoring == MOE_SCORE_SOFTMAX ? 0x1p-18f : 0x1.4p-19f;
+        // In units of 2^-23 of the largest magnitude in play: by the library's
+        // bounds (exp 3, log1p 2, sqrt 3, division 2.5 last bits) a float32 score
+        // is within 6.5 of the exact one, and the roundings of the scores and of
+        // their sums with the bias add 1.5 a side: 16 for the two sides of a
+        // comparison.  A softmax's sum is off by 14 at most (exp 3, 14
+        // additions 7, the differences' roundings, weighted by the terms, 4) on
+        // both sides alike, so this adds 14 times the two scores' difference: 30.
+        // A rank of two scores doubles all of it and adds 4 for its own roundings.
+        // (Scores below 2^-126: 2^-149 absolute.)
+        constexpr float kMargin = scoring == MOE_SCORE_SOFTMAX ? 0x1.1p-18f : 0x1.4p-19f;
         float big = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {

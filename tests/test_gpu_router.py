@@ -190,3 +190,31 @@ def test_captured_and_replayed():
         call()
         torch.cuda.synchronize()
         assert torch.equal(got[0], ids) and torch.equal(got[1], w)
+
+
+def masked_top_rows(n, seed):
+    """Rows whose largest logit is 70 above the rest and masked by the bias, so
+    that every score in play is below 2^-90; the four experts left lie within
+    2^-25 of a place half way between two float32 values of logit - 70 (2^-17
+    apart), on either side of it."""
+    rng = np.random.default_rng(seed)
+    rows = np.empty((n, 6))
+    rows[:, 0], rows[:, 1] = 70.0, -5.0
+    place = rng.choice([-1, 1], size=(n, 1)) * (rng.integers(0, 512, size=(n, 1)) + 0.5) * 2.0 ** -17
+    rows[:, 2:] = place + rng.integers(-32, 33, size=(n, 4)) * 2.0 ** -30
+    return rows
+
+
+def test_largest_logit_masked_by_the_bias():
+    """The scores' differences then hang on the rounding of logit - largest."""
+    log("[test] router, largest logit masked by the bias")
+    ninf = -math.inf
+    one = np.array([[70, float.fromhex("0x1.73bffep-8"), float.fromhex("0x1.73c002p-8"), -3]])
+    check(one, 1, "softmax", np.array([ninf, 0, 0, 0], np.float32))
+    two = np.array([[70, -5, 0.9967848062515259, 0.996761679649353, 0.9967756867408752, 0.9967743158340454]])
+    check(two, 2, "softmax", np.array([ninf, ninf, 0, 0, 0, 0], np.float32), 3, 1)
+    x = masked_top_rows(4000, 6)
+    check(x, 1, "softmax", np.array([ninf, 0, 0, 0, 0, 0], np.float32))
+    check(x, 3, "softmax", np.array([math.nan, 0, 0, 0, 0, 0], np.float32))
+    check(x, 2, "softmax", np.array([ninf, ninf, 0, 0, 0, 0], np.float32), 3, 1)
+    check(x, 2, "softmax", np.array([ninf, 0, 0, 0, 0, 0], np.float32), 3, 2)
