@@ -316,7 +316,7 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1, MOE_SCORE_SQRTSOFTPLUS = 2 
 
 /* The router's choice: topk_ids and topk_weights of every forward from the
  * logits of the num_experts experts.  Per token:
- *   s[e]   = score of logit l[e], computed in fp64 and rounded to float32;
+ *   s[e]   = score of logit l[e], of the fp64 value rounded to float32;
  *   c[e]   = l[e] when bias is NULL (every scoring rises with the logit), else
  *            s[e] + bias[e] in float32;
  *   groups: experts [j*num_experts/num_groups, ...) are group j; its rank is its
@@ -327,6 +327,9 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1, MOE_SCORE_SQRTSOFTPLUS = 2 
  *            equal ones (groups too) by the lower index;
  *   weights = s[ids], divided by (their sum + 1e-20) when renormalize is not
  *            0, times scale.
+ * The ids are exactly these.  The weights are computed in float32, a softmax's
+ * sum included: within 2^-18 of the value defined here (a score below 2^-126:
+ * within 2^-149, before the division and the scale).
  * An expert whose logit or c is -infinity or NaN is not chosen (masked or out
  * of service).  Slots for which no expert is left get id -1 and weight 0: a
  * forward skips them.  A logit of +infinity counts as the largest float.

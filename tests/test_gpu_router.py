@@ -218,3 +218,16 @@ def test_largest_logit_masked_by_the_bias():
     check(x, 3, "softmax", np.array([math.nan, 0, 0, 0, 0, 0], np.float32))
     check(x, 2, "softmax", np.array([ninf, ninf, 0, 0, 0, 0], np.float32), 3, 1)
     check(x, 2, "softmax", np.array([ninf, 0, 0, 0, 0, 0], np.float32), 3, 2)
+
+
+def test_softmax_weights_far_below_the_largest_logit():
+    """logit - largest at half a step of float32 between 64 and 87: the weights
+    keep the bound of the nearer ones."""
+    log("[test] router, softmax weights far below the largest")
+    rng = np.random.default_rng(7)
+    x = np.full((600, 4), -200.0)
+    x[:, 0] = 70.0
+    steps = rng.integers(0, 1 << 15, size=(600, 2)) * 2.0 ** -17
+    x[:, 1:3] = rng.choice([-1, 1], size=(600, 2)) * (steps + 2.0 ** -18 - 2.0 ** -26)     # exact in float32
+    check(x, 3, "softmax", renorm=False)
+    check(x, 2, "softmax", np.array([-math.inf, 0, 0, 0], np.float32), renorm=False, scale=2.0 ** 60)
