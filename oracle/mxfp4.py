@@ -30,18 +30,21 @@ SCALE_EXP_MIN = -127
 SCALE_EXP_MAX = 127
 
 
+# Value of every 4-bit code, and of the two codes of every byte (low nibble first).
+E2M1_VALUES = np.concatenate([E2M1_MAGNITUDES, -E2M1_MAGNITUDES])
+_PAIRS = np.stack([np.tile(E2M1_VALUES, 16), np.repeat(E2M1_VALUES, 16)], axis=-1)
+# Value 2^(b-127) of every scale byte; NaN for 255.
+_SCALES = np.append(np.ldexp(1.0, np.arange(255) - 127), np.nan)
+
+
 def e2m1_decode(codes) -> np.ndarray:
     """fp64 value of each 4-bit code ([OCP-MX] E2M1)."""
-    c = np.asarray(codes).astype(np.int64)
-    mag = E2M1_MAGNITUDES[c & 7]
-    return np.where((c >> 3) & 1, -mag, mag)
+    return E2M1_VALUES[np.asarray(codes) & 15]
 
 
 def ue8m0_decode(b) -> np.ndarray:
     """fp64 value 2^(b-127) of each scale byte; NaN for 255 ([OCP-MX] E8M0)."""
-    b = np.asarray(b).astype(np.int64)
-    v = np.ldexp(1.0, b - 127)
-    return np.where(b == 255, np.nan, v)
+    return _SCALES[np.asarray(b)]
 
 
 def scale_exponent(amax) -> np.ndarray:
@@ -64,23 +67,26 @@ def scale_exponent(amax) -> np.ndarray:
     return np.clip(e, SCALE_EXP_MIN, SCALE_EXP_MAX)
 
 
+# Midpoints of neighbouring magnitudes, and whether a value on one goes up: to the
+# neighbour whose index (mantissa bit) is even.
+_MIDPOINTS = [((lo + hi) / 2, up % 2 == 0)
+              for up, (lo, hi) in enumerate(zip(E2M1_MAGNITUDES[:-1], E2M1_MAGNITUDES[1:]), 1)]
+
+
 def round_to_e2m1(r) -> np.ndarray:
     """Nearest E2M1 code for each (already scaled) value; ties to the even code.
 
-    The magnitude index is the arg-min of |  |r| - table  | over the 8 table
-    entries; on a tie between two adjacent entries the even index (mantissa
-    bit 0) wins.  Sign bit copied from r.
+    The magnitude index is the number of midpoints of neighbouring table entries
+    that |r| has passed; on a midpoint the even index (mantissa bit 0) wins.
+    Sign bit copied from r.
     """
     r = np.asarray(r, dtype=np.float64)
     mag = np.abs(r)
     assert np.all(mag <= E2M1_MAX), "scaled value outside the E2M1 range"
-    d = np.abs(mag[..., None] - E2M1_MAGNITUDES)            # [..., 8]
-    dmin = d.min(axis=-1, keepdims=True)
-    cand = d == dmin
-    even = cand & (np.arange(8) % 2 == 0)
-    idx = np.where(even.any(axis=-1), even.argmax(axis=-1), cand.argmax(axis=-1))
-    sign = np.signbit(r).astype(np.int64)
-    return (idx | (sign << 3)).astype(np.uint8)
+    idx = np.signbit(r).astype(np.uint8) << 3
+    for mid, tie_up in _MIDPOINTS:
+        idx += (mag >= mid) if tie_up else (mag > mid)
+    return idx
 
 
 def quantize(v, chunk_rows: int = 1 << 14):
@@ -100,7 +106,7 @@ def quantize(v, chunk_rows: int = 1 << 14):
     for s in range(0, flat.shape[0], chunk_rows):
         blk = flat[s:s + chunk_rows]
         e = scale_exponent(np.abs(blk).max(axis=-1))
-        r = np.ldexp(blk, -e[..., None])                      # exact: power-of-two scaling
+        r = blk * np.ldexp(1.0, -e)[..., None]                # exact: power-of-two scaling
         codes[s:s + chunk_rows] = round_to_e2m1(r)
         scales[s:s + chunk_rows] = (e + 127).astype(np.uint8)
     return codes.reshape(*lead, K), scales.reshape(*lead, K // GROUP)
@@ -129,7 +135,9 @@ def quantize_packed(v):
 
 def dequantize(packed, scales) -> np.ndarray:
     """fp64 values [..., K] of packed codes [..., K/2] with scale bytes [..., K/32]."""
-    vals = e2m1_decode(unpack(packed))
-    K = vals.shape[-1]
-    sc = ue8m0_decode(scales)
-    return (vals.reshape(*vals.shape[:-1], K // GROUP, GROUP) * sc[..., None]).reshape(vals.shape)
+    p = np.asarray(packed)
+    # one 16-byte entry a byte of codes (the complex view moves a pair at a time)
+    vals = np.take(_PAIRS.view(np.complex128)[:, 0], p).view(np.float64)
+    grouped = vals.reshape(*p.shape[:-1], -1, GROUP)
+    grouped *= ue8m0_decode(scales)[..., None]
+    return vals

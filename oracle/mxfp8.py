@@ -33,14 +33,21 @@ SCALE_EXP_MIN = -127
 SCALE_EXP_MAX = 127
 
 
-def e4m3_decode(codes) -> np.ndarray:
+def _decode_fields(c) -> np.ndarray:
     """fp64 value of each 8-bit code, from its bit fields ([OCP-MX] E4M3)."""
-    c = np.asarray(codes).astype(np.int64)
     ex = (c >> 3) & 15
     m = (c & 7).astype(np.float64)
     mag = np.where(ex == 0, np.ldexp(m / 8.0, -6), np.ldexp(1.0 + m / 8.0, ex - 7))
     mag = np.where((c & 0x7F) == 0x7F, np.nan, mag)
     return np.where((c >> 7) & 1, -mag, mag)
+
+
+E4M3_VALUES = _decode_fields(np.arange(256))
+
+
+def e4m3_decode(codes) -> np.ndarray:
+    """fp64 value of each 8-bit code."""
+    return E4M3_VALUES[np.asarray(codes)]
 
 
 # Magnitudes of the non-negative finite codes 0x00 .. 0x7E, in code order
@@ -105,7 +112,7 @@ def quantize(v, chunk_rows: int = 1 << 14):
     for s in range(0, flat.shape[0], chunk_rows):
         blk = flat[s:s + chunk_rows]
         e = scale_exponent(np.abs(blk).max(axis=-1))
-        r = np.ldexp(blk, -e[..., None])                      # exact: power-of-two scaling
+        r = blk * np.ldexp(1.0, -e)[..., None]                # exact: power-of-two scaling
         codes[s:s + chunk_rows] = round_to_e4m3(r)
         scales[s:s + chunk_rows] = (e + 127).astype(np.uint8)
     return codes.reshape(*lead, K), scales.reshape(*lead, K // GROUP)
