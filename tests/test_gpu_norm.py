@@ -236,3 +236,16 @@ def test_many_long_rows(rows, cols, res, mma):
     rng = np.random.default_rng(rows + cols)
     r = None if res is None else rng.normal(size=(rows, cols))
     check(make(rows, cols, cols), r, res, np.exp(0.3 * rng.normal(size=cols)), False, mma, inplace=rows == 300)
+
+
+@pytest.mark.parametrize("cols", [512, 4096, 16384])
+def test_y_in_the_place_of_a_bf16_residual(cols):
+    log(f"[test] norm y over the residual, cols {cols}")
+    x, r = dev_bf16(make(300, cols, 24)), dev_bf16(make(300, cols, 25))
+    w = torch.linspace(0.5, 2.0, cols, device="cuda")
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    _lib.moe_w4a4_add_rmsnorm(x, r, w, EPS, residual_out=h, y=y)
+    h2 = torch.empty_like(x)
+    _lib.moe_w4a4_add_rmsnorm(x, r, w, EPS, residual_out=h2, y=r)
+    torch.cuda.synchronize()
+    assert torch.equal(h2, h) and torch.equal(r, y)
