@@ -2,6 +2,10 @@
 
 Tolerance: oracle.linear.sum_error (the matrix cores' sums), then half a step
 of the output's type: 2^-8 (bfloat16), 2^-24 (float32) of the value."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -327,3 +331,46 @@ def test_few_tokens(T, K, N, mma):
     a = bf16.decode(add)
     plus = run(lin, x, T, N, dtype=torch.float32, addend=dev_bf16(add))
     close(plus.double().cpu().numpy(), ref + a, mag + np.abs(a), K, mma, f32=True)
+
+
+# one size for each kernel that needs more LDS than a launch has by default
+CAPTURED_FIRST = [(1, 8192, 100, "decode"), (500, 288, 3001, "64 tokens"), (2000, 640, 2048, "128 tokens"),
+                  (4100, 96, 4097, "256 rows")]
+FRESH_PROCESS = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from tests.test_gpu_linear import CAPTURED_FIRST, FP8, MX4, dev_bf16, make_linear, tokens, weights
+for mma in (MX4, FP8):
+    for T, K, N, plan in CAPTURED_FIRST:
+        lin = make_linear(K, N, T, mma, *weights(N, K, 51))
+        xs = [dev_bf16(tokens(T, K, s)) for s in (52, 53)]
+        x, out = xs[0].clone(), torch.zeros((T, N), dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lin.forward(x, out=out)              # the process's first call of this kernel
+        for i in (1, 0, 1):
+            x.copy_(xs[i])
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, lin.forward(xs[i])), (mma, plan)
+        assert torch.count_nonzero(out).item() > T * N // 2
+        print("captured first:", mma, plan, flush=True)
+"""
+
+
+def test_every_kernels_first_call_inside_a_capture():
+    """In a process of its own, where no launch limit was raised before."""
+    log("[test] linear kernels captured first, in a fresh process")
+    for T, K, N, plan in CAPTURED_FIRST:         # launch_ops.h's linear_plan
+        steps, t64, t128, n128, n256 = -(-K // 128), -(-T // 64), -(-T // 128), -(-N // 128), -(-N // 256)
+        if plan == "decode":                     # more than 64 KiB of operands and sums in LDS
+            assert 32 < steps <= 64 and T == 1 and N <= 256 * 16 and steps * (1024 + 64) + 16384 > 65536
+        else:
+            assert T > 16 and t64 * n128 > 128
+            assert plan == ("64 tokens" if t64 * n128 <= 256 else "256 rows" if t128 * n256 >= 512 else "128 tokens")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-u", "-c", FRESH_PROCESS.format(root=root)], cwd=root, capture_output=True,
+                       text=True, timeout=110)
+    print(r.stdout)
+    assert r.returncode == 0 and r.stdout.count("captured first:") == 2 * len(CAPTURED_FIRST), r.stdout + r.stderr
