@@ -20,6 +20,19 @@ import torch
 from . import _lib
 
 
+def _output(shape, dtype, device, stream):
+    """A new tensor for a call to fill on `stream` (None: the current stream).
+    It is of that stream's memory: the current stream's own free blocks may have
+    pending work of that stream on them.  The caller reads it on the current
+    stream, so its memory waits for that one too before it is used again."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device)):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 class MoeW4A4Layer:
     PREDISPATCH_ROWS = 8192      # routed rows up to which a forward quantizes and routes in one launch
 
@@ -126,7 +139,7 @@ class MoeW4A4Layer:
         kernel is launched."""
         T = x.shape[0]
         if out is None:
-            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
+            out = _output((T, self.H), torch.bfloat16, self.device, stream)
         with torch.cuda.device(self.device):
             _lib.moe_w4a4_forward(self.cfg, self.prepared, T, x, topk_ids, topk_weights, out, self.workspace,
                                   stream=stream)
@@ -137,7 +150,7 @@ class MoeW4A4Layer:
         fp8xfp4, at most 256 routed rows); arguments as forward."""
         T = x.shape[0]
         if out is None:
-            out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
+            out = _output((T, self.H), torch.bfloat16, self.device, stream)
         with torch.cuda.device(self.device):
             _lib.moe_w4a4_forward_mega(self.cfg, self.prepared, T, x, topk_ids, topk_weights, out, self.workspace,
                                        stream=stream)
@@ -164,11 +177,11 @@ class MoeW4A4Layer:
             raise ValueError(f"x: {T} tokens, the layer holds {self.max_tokens}")
         on_stream = torch.cuda.stream(torch.cuda.ExternalStream(int(stream), self.device)) if stream is not None \
             else contextlib.nullcontext()
+        if residual_out is None and residual is not None:
+            residual_out = _output(residual.shape, residual.dtype, self.device, stream)
+        if out is None:
+            out = _output((T, self.H), torch.bfloat16, self.device, stream)
         with torch.cuda.device(self.device), on_stream:
-            if residual_out is None and residual is not None:
-                residual_out = torch.empty_like(residual)
-            if out is None:
-                out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
             y = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
             ids = torch.empty((T, self.k), dtype=torch.int32, device=self.device)
             weights = torch.empty((T, self.k), dtype=torch.float32, device=self.device)
@@ -259,7 +272,7 @@ class W4A4Linear:
     def _run(self, x, xq, xsf, out, addend, dtype, stream):
         if out is None:
             T = (x if x is not None else xq).shape[0]
-            out = torch.empty((T, self.N), dtype=dtype, device=self.device)
+            out = _output((T, self.N), dtype, self.device, stream)
         index = self.device.index
         if torch._C._cuda_getDevice() != index:
             with torch.cuda.device(index):

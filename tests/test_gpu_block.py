@@ -155,3 +155,37 @@ def test_linears_on_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for w, o in zip(want, outs):
         assert all(torch.equal(w, t) for t in o)
+
+
+def on_another_stream(call):
+    """call(stream) -> new output tensors, filled on another stream while the
+    current one still has to read memory that was freed after it: the outputs
+    must not lie there."""
+    side = torch.cuda.Stream()
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    held = [torch.full_like(t, 3.0) for t in want]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                     # the current stream is busy for a while
+    kept = [t.clone() for t in held]
+    places = [t.data_ptr() for t in held]
+    del held
+    got = call(side.cuda_stream)
+    assert not {t.data_ptr() for t in got} & set(places)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(bool((t == 3.0).all()) for t in kept)
+
+
+@pytest.mark.parametrize("T", [5, 300])
+def test_new_outputs_are_of_the_streams_own_memory(T):
+    log(f"[test] T {T}: outputs made for another stream")
+    layer, shared, _, gate = block(T, MX4)
+    x, r, w, b = (dev_bf16(v) if v.dtype == np.uint16 else dev(v) for v in inputs(T, 9))
+    gd = dev_bf16(gate)
+    ids = torch.arange(T * K, dtype=torch.int32, device="cuda").view(T, K) % E
+    rw = torch.full((T, K), 0.5, device="cuda")
+    on_another_stream(lambda s: [shared.forward(x, stream=s)])
+    on_another_stream(lambda s: [shared.forward(x, dtype=torch.float32, stream=s)])
+    on_another_stream(lambda s: [layer.forward(x, ids, rw, stream=s)])
+    on_another_stream(lambda s: list(layer.forward_block(x, r, w, 1e-6, gd, bias=b, shared=shared, stream=s, **ROUTE)))
