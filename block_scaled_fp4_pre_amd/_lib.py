@@ -324,10 +324,10 @@ def _raw_stream(stream, device_index: int) -> int:
     return int(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(device_index)
 
 
-def _fits(t, name: str, dtypes, shape, device_index: int) -> int:
-    """Device address of a contiguous tensor of one of the dtypes, of that
+def _fits(t, name: str, dtypes, shape, device_index: int, contiguous: bool = True) -> int:
+    """Device address of a (contiguous) tensor of one of the dtypes, of that
     shape, on device `device_index`; else ValueError."""
-    if t.dtype in dtypes and t.shape == shape and t.get_device() == device_index and t.is_contiguous():
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == device_index and (t.is_contiguous() or not contiguous):
         return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
@@ -337,7 +337,7 @@ def _fits(t, name: str, dtypes, shape, device_index: int) -> int:
         raise ValueError(f"{name}: expected a device tensor, got one on {t.device}")
     if t.device.index != device_index:
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device_index}")
-    if not t.is_contiguous():
+    if contiguous and not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
     return t.data_ptr()
 
@@ -411,6 +411,14 @@ def moe_w4a4_router(logits, topk_ids, topk_weights, bias=None, scoring: int = MO
                               pb, 1 if renormalize else 0, scale, pi, pw, _raw_stream(stream, dev))
     if st != MOE_OK:
         raise MoeError(st, "moe_w4a4_router")
+
+
+def _check_router_config(num_experts: int, topk: int, scoring: int, num_groups: int, topk_groups: int,
+                         scale: float) -> None:
+    """Raise what moe_w4a4_router would raise for its plain arguments (the library
+    checks them for no tokens too)."""
+    _check(_lib.moe_w4a4_router(1, scoring, 0, num_experts, topk, num_groups, topk_groups, None, None, 1, scale, None,
+                                None, None), "moe_w4a4_router")
 
 
 def make_linear_cfg(in_features: int, out_features: int, max_tokens: int,

@@ -157,6 +157,36 @@ class MoeW4A4Layer:
         return out
 
     # ---- the layer with what feeds it ----------------------------------------
+    def _check_block(self, T, gate, bias, scoring, num_groups, topk_groups, scale, shared, residual_out, out) -> None:
+        """Everything that the steps behind the norm would refuse: the norm may
+        overwrite x and the residual, so the others' arguments are checked first."""
+        H, E, dev = self.H, self.E, self.device.index
+        if T > self.max_tokens:
+            raise ValueError(f"x: {T} tokens, the layer holds {self.max_tokens}")
+        for name, lin, n in (("gate_weight", gate, E), ("shared", shared, H)):
+            if not isinstance(lin, W4A4Linear):
+                continue
+            if (lin.K, lin.N, lin.device) != (H, n, self.device):
+                raise ValueError(f"{name}: from {lin.K} to {lin.N} on {lin.device}, expected {H} to {n} on {self.device}")
+            if lin.max_tokens < T:
+                raise ValueError(f"{name}: holds {lin.max_tokens} tokens, not {T}")
+        if not isinstance(gate, W4A4Linear):
+            _lib._fits(gate, "gate_weight", (torch.bfloat16,), (E, H), dev, contiguous=False)
+        if shared is not None and not isinstance(shared, W4A4Linear):
+            raise ValueError(f"shared: expected a W4A4Linear, got {type(shared).__name__}")
+        _lib._check_router_config(E, self.k, scoring, num_groups, topk_groups, scale)
+        if bias is not None:
+            _lib._fits(bias, "bias", (torch.float32,), (E,), dev)
+        if out is not None:
+            # (a forward alone takes more rows, and bit patterns)
+            rows = T if shared is not None else max(T, out.shape[0] if out.dim() == 2 else 0)
+            types = (torch.bfloat16,) if shared is not None else (torch.bfloat16, torch.int16, torch.uint16)
+            place = _lib._fits(out, "out", types, (rows, H), dev)
+            if place % 16:
+                raise ValueError("out: not 16-byte aligned")
+            if residual_out is not None and place == residual_out.data_ptr() and T > 0:
+                raise ValueError("out: in the place of residual_out")
+
     def forward_block(self, x, residual, norm_weight, eps, gate_weight, residual_out=None, bias=None,
                       scoring=_lib.MOE_SCORE_SOFTMAX, num_groups=1, topk_groups=1, renormalize=True, scale=1.0,
                       shared=None, out=None, stream=None):
@@ -173,8 +203,7 @@ class MoeW4A4Layer:
         pre-dispatch (more than 8192 routed rows) are quantized by the norm,
         into the workspace, and not read again by a quantizer."""
         T = x.shape[0]
-        if T > self.max_tokens:
-            raise ValueError(f"x: {T} tokens, the layer holds {self.max_tokens}")
+        self._check_block(T, gate_weight, bias, scoring, num_groups, topk_groups, scale, shared, residual_out, out)
         on_stream = torch.cuda.stream(torch.cuda.ExternalStream(int(stream), self.device)) if stream is not None \
             else contextlib.nullcontext()
         if residual_out is None and residual is not None:

@@ -155,3 +155,50 @@ def test_linear_refuses_shared_weights_with_gaps():
     for bad in (_t((2 * pb,), U8)[::2], _t((pb - 1,), U8), _t((1,), U8).expand(pb)):
         with pytest.raises(ValueError, match="prepared"):
             W4A4Linear(64, 32, 8, "cuda:0", prepared=bad)
+
+
+def _block_layer():
+    from block_scaled_fp4_pre_amd.layer import MoeW4A4Layer
+    layer = MoeW4A4Layer.__new__(MoeW4A4Layer)
+    layer.H, layer.I, layer.E, layer.k, layer.max_tokens = 64, 64, 16, 3, 8
+    layer.mma_type, layer.device = _lib.MOE_MMA_MXF4_X_MXF4, torch.device("cuda", 0)
+    return layer
+
+
+def _block_linear(K, N, max_tokens, index=0):
+    from block_scaled_fp4_pre_amd.layer import W4A4Linear
+    lin = W4A4Linear.__new__(W4A4Linear)
+    lin.K, lin.N, lin.max_tokens, lin.device = K, N, max_tokens, torch.device("cuda", index)
+    return lin
+
+
+# what a step behind the norm would refuse
+BLOCK_REFUSALS = [
+    dict(gate_weight=_t((16, 64), F32)), dict(gate_weight=_t((15, 64))), dict(gate_weight=_t((16, 32))),
+    dict(gate_weight=torch.zeros((16, 64), dtype=BF)), dict(gate_weight=_block_linear(64, 16, 3)),
+    dict(gate_weight=_block_linear(64, 17, 8)), dict(gate_weight=_block_linear(64, 16, 8, 1)),
+    dict(bias=_t((15,), F32)), dict(bias=_t((16,))), dict(scoring=3), dict(num_groups=5), dict(num_groups=4, topk_groups=5),
+    dict(num_groups=8, topk_groups=1), dict(scale=float("inf")), dict(scale=float("nan")),
+    dict(shared=_block_linear(64, 64, 3)), dict(shared=_block_linear(64, 32, 8)), dict(shared=_block_linear(32, 64, 8)),
+    dict(shared=_block_linear(64, 64, 8, 1)), dict(shared=_t((64, 64))), dict(out=_t((4, 32))), dict(out=_t((3, 64))),
+    dict(out=_t((4, 64), F32)), dict(out=_t((64, 4)).t()), dict(out=_t((5, 64)), shared=_block_linear(64, 64, 8)),
+    dict(out=_t((1, 257))[:, 1:].reshape(4, 64))]
+
+
+@pytest.mark.parametrize("change", BLOCK_REFUSALS, ids=lambda c: ",".join(f"{k}{i}" for i, k in enumerate(c)))
+def test_block_refuses_before_the_norm(monkeypatch, change):
+    def reached(*a, **k):
+        raise AssertionError("the norm was called")
+    monkeypatch.setattr(_lib, "moe_w4a4_add_rmsnorm", reached)
+    a = dict(x=_t((4, 64)), residual=_t((4, 64)), norm_weight=_t((64,), F32), eps=1e-6, gate_weight=_t((16, 64)))
+    with pytest.raises((ValueError, _lib.MoeError)):
+        _block_layer().forward_block(**{**a, **change})
+
+
+def test_block_refuses_an_output_in_the_place_of_the_residual():
+    a = dict(x=_t((4, 64)), norm_weight=_t((64,), F32), eps=1e-6, gate_weight=_t((16, 64)))
+    r = _t((4, 64))
+    with pytest.raises(ValueError, match="residual_out"):
+        _block_layer().forward_block(residual=r, residual_out=r, out=r, **a)
+    with pytest.raises(ValueError, match="holds"):
+        _block_layer().forward_block(residual=None, **{**a, "x": _t((9, 64))})
