@@ -20,6 +20,13 @@ import torch
 from . import _lib
 
 
+def _torch_stream(stream, device):
+    """torch's stream of a raw handle.  0 is the default stream's (torch would take
+    an external stream of handle 0 to mean a new stream of its pool)."""
+    handle = int(stream)
+    return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+
+
 def _output(shape, dtype, device, stream):
     """A new tensor for a call to fill on `stream` (None: the current stream).
     It is of that stream's memory: the current stream's own free blocks may have
@@ -27,7 +34,7 @@ def _output(shape, dtype, device, stream):
     stream, so its memory waits for that one too before it is used again."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device)):
+    with torch.cuda.stream(_torch_stream(stream, device)):
         out = torch.empty(shape, dtype=dtype, device=device)
     out.record_stream(torch.cuda.current_stream(device))
     return out
@@ -204,8 +211,7 @@ class MoeW4A4Layer:
         into the workspace, and not read again by a quantizer."""
         T = x.shape[0]
         self._check_block(T, gate_weight, bias, scoring, num_groups, topk_groups, scale, shared, residual_out, out)
-        on_stream = torch.cuda.stream(torch.cuda.ExternalStream(int(stream), self.device)) if stream is not None \
-            else contextlib.nullcontext()
+        on_stream = contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream, self.device))
         if residual_out is None and residual is not None:
             residual_out = _output(residual.shape, residual.dtype, self.device, stream)
         if out is None:

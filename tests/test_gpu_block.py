@@ -189,3 +189,28 @@ def test_new_outputs_are_of_the_streams_own_memory(T):
     on_another_stream(lambda s: [shared.forward(x, dtype=torch.float32, stream=s)])
     on_another_stream(lambda s: [layer.forward(x, ids, rw, stream=s)])
     on_another_stream(lambda s: list(layer.forward_block(x, r, w, 1e-6, gd, bias=b, shared=shared, stream=s, **ROUTE)))
+
+
+@pytest.mark.parametrize("T", [5, 2800])
+def test_handle_of_the_default_stream(T):
+    """stream=0, which is what torch's default stream has for a handle: the call
+    follows what that stream still has to do."""
+    log(f"[test] block T {T} on the default stream by its handle")
+    layer, shared, _, gate = block(T, MX4)
+    x, r, w, b = (dev_bf16(v) if v.dtype == np.uint16 else dev(v) for v in inputs(T, 10))
+    gd, late = dev_bf16(gate), torch.zeros_like(x)
+    assert torch.cuda.current_stream().cuda_stream == 0
+    want = layer.forward_block(x, r, w, 1e-6, gd, bias=b, shared=shared, **ROUTE)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    late.copy_(x)
+    got = layer.forward_block(late, r, w, 1e-6, gd, bias=b, shared=shared, stream=0, **ROUTE)
+    lin = shared.forward(late, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(lin, shared.forward(x))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):                # also where another stream is the current one
+        again = layer.forward_block(late, r, w, 1e-6, gd, bias=b, shared=shared, stream=0, **ROUTE)
+    torch.cuda.synchronize()
+    assert torch.equal(again[0], want[0])
