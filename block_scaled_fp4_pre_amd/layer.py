@@ -203,12 +203,17 @@ class MoeW4A4Layer:
         one.  Returns (out, h): out = experts(y) (+ shared(y)) bf16 [T, H], and
         the new residual stream h = x + residual, of the residual's type.
         x bf16 [T, H]; residual bf16 / float32 [T, H] (residual_out like it,
-        may be it; a new tensor if None), or None (h is x then); norm_weight [H]; gate_weight [E, H]
-        bf16 (logits by a plain product), or a W4A4Linear with out_features E;
-        bias float32 [E]; shared: a W4A4Linear from H to H, added to the
-        experts' output before its rounding.  Tokens past the fused
-        pre-dispatch (more than 8192 routed rows) are quantized by the norm,
-        into the workspace, and not read again by a quantizer."""
+        may be it; a new tensor if None), or None (h is x then); norm_weight [H].
+        gate_weight: bf16 [E, H], whose logits are torch's own product and so
+        rounded to bf16 before the choice; or a W4A4Linear with out_features E,
+        whose logits are float32.  bias float32 [E].
+        shared: one W4A4Linear from H to H (no activation), whose sum is added
+        to the experts' output, that one rounded to bf16, and rounded again.
+        Past the fused pre-dispatch (more than 8192 routed rows) the norm
+        quantizes y into the workspace and the experts start from that; a
+        W4A4Linear gate and `shared` quantize y for themselves.
+        Arguments that any step would refuse raise before the first launch, with
+        x and residual as they were."""
         T = x.shape[0]
         self._check_block(T, gate_weight, bias, scoring, num_groups, topk_groups, scale, shared, residual_out, out)
         on_stream = contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream, self.device))
@@ -260,7 +265,9 @@ class MoeW4A4Layer:
 
 class W4A4Linear:
     """A dense linear with MXFP4 weights (moe_w4a4_linear): owns the prepared
-    weights and the workspace for max_tokens tokens."""
+    weights and the workspace for max_tokens tokens.  Calls that may run at the
+    same time (on two streams, or in two captured graphs) need a linear each
+    (with_capacity): they would share the workspace."""
 
     def __init__(self, in_features: int, out_features: int, max_tokens: int,
                  device: str | torch.device = "cuda", mma_type: int = _lib.MOE_MMA_MXF4_X_MXF4,
