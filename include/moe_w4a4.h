@@ -301,9 +301,9 @@ int moe_w4a4_forward_noalloc(const moe_w4a4_cfg* cfg, const void* prepared, int3
  * has the address of another, or of an input that it may not be).
  * cols % 32 == 0, cols <= 65536, rows >= 0 (0 enqueues nothing and looks at no
  * pointer), eps finite and > 0; without codes mma_type and g are not looked
- * at.  y or codes must be given.  Values must be finite, and so must x + residual: a row with others
- * gets a y with NaN or infinity in it and unspecified codes; other rows are
- * untouched by it.  xq and xsf of the forward's workspace may be the codes and
+ * at.  y or codes must be given.  Values must be finite, and so must x + residual
+ * and y: a row with others gets a y with NaN or infinity in it and unspecified
+ * codes; other rows are untouched by it.  xq and xsf of the forward's workspace may be the codes and
  * scales here: moe_w4a4_run_stages without MOE_STAGE_QUANT then starts from
  * them. */
 int moe_w4a4_add_rmsnorm(int32_t mma_type, int32_t res_dtype, int32_t w_dtype, int64_t rows, int32_t cols,
@@ -339,7 +339,8 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1, MOE_SCORE_SQRTSOFTPLUS = 2 
  *   bias          NULL, or device float32 [num_experts]
  *   topk_ids      device int32 [num_tokens, topk]
  *   topk_weights  device float32 [num_tokens, topk]
- * All aligned to their element size.  1 <= num_experts <= 512, 1 <= topk <= 16,
+ * All aligned to their element size; the outputs overlap neither each other nor
+ * an input.  1 <= num_experts <= 512, 1 <= topk <= 16,
  * num_groups (at most 64) divides num_experts, 1 <= topk_groups <= num_groups,
  * topk <= topk_groups * (num_experts / num_groups), scale finite; num_tokens >=
  * 0 (0 enqueues nothing and looks at no pointer) and num_tokens * num_experts
@@ -370,7 +371,7 @@ int moe_w4a4_linear_query(const moe_w4a4_linear_cfg* cfg, size_t* prepared_bytes
  * scales uint8 [N, K/32]; device) into the operand order of the product, once
  * at load time: a byte permutation, with zeros where N and K are padded to
  * whole tiles.  prepared: device buffer of query's prepared_bytes, 256-byte
- * aligned. */
+ * aligned, apart from the two. */
 int moe_w4a4_linear_prepare(const moe_w4a4_linear_cfg* cfg, const uint8_t* codes, const uint8_t* scales,
                             void* prepared, size_t prepared_bytes, void* stream);
 

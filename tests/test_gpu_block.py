@@ -214,3 +214,35 @@ def test_handle_of_the_default_stream(T):
         again = layer.forward_block(late, r, w, 1e-6, gd, bias=b, shared=shared, stream=0, **ROUTE)
     torch.cuda.synchronize()
     assert torch.equal(again[0], want[0])
+
+
+@pytest.mark.parametrize("mma", [MX4, FP8, _lib.MOE_MMA_NVF4_X_NVF4], ids=["mxf4xmxf4", "fp8xfp4", "nvf4xnvf4"])
+@pytest.mark.parametrize("res", [None, "bf16", "f32"])
+def test_block_equals_its_steps(mma, res):
+    """Every type and residual, no tokens among the counts: the bits of the
+    steps called one by one."""
+    log(f"[test] block type {mma} residual {res}")
+    T = 2800
+    if mma == _lib.MOE_MMA_NVF4_X_NVF4:
+        layer = layer_for(H, I, E, K, T, mma_type=mma)
+        scales = np.full(E, 2.0 ** -14, np.float32)
+        layer.load_fp32(lambda e: synth.expert_weights_f32(config(T), e), threads=4,
+                        tensor_scales=(2.0 ** -8, 2.0 ** -8, scales, scales))
+        shared = block(T, MX4)[1]
+        gate = block(T, MX4)[3]
+    else:
+        layer, shared, _, gate = block(T, mma)
+    x, r, w, b = (dev_bf16(v) if v.dtype == np.uint16 else dev(v) for v in inputs(T, 12))
+    gd = dev_bf16(gate).t().contiguous().t()              # a gate stored the other way round
+    r = None if res is None else r.float() * 1.001 if res == "f32" else r
+    for n in (0, 1, 40, T):
+        rn = None if r is None else r[:n].clone()
+        out, h = layer.forward_block(x[:n], rn, w, 1e-6, gd, bias=b, shared=shared, **ROUTE)
+        y, ro = torch.empty_like(x[:n]), None if r is None else torch.empty_like(rn)
+        _lib.moe_w4a4_add_rmsnorm(x[:n], rn, w, 1e-6, residual_out=ro, y=y)
+        ids, rw = torch.empty((n, K), dtype=torch.int32, device="cuda"), torch.empty((n, K), device="cuda")
+        _lib.moe_w4a4_router(torch.nn.functional.linear(y, gd), ids, rw, bias=b, **ROUTE)
+        want = shared.forward(y, addend=layer.forward(y, ids, rw))
+        torch.cuda.synchronize()
+        assert out.shape == (n, H) and torch.equal(out, want)
+        assert h is x[:n] or torch.equal(h, x[:n] if r is None else ro)
