@@ -189,7 +189,7 @@ def cpu_baseline(cfg, x, ids, w, mma_type="mxf4xmxf4", weight_pool=2):
     are load-time work and are not timed; the oracle quantizes weight_pool
     experts' weights and every expert uses one of them in turn (its arithmetic
     and cost do not depend on the weight values, and quantizing all 256
-    experts' 3.4 GB with the oracle's brute-force quantizer would take tens of
+    experts' 3.4 GB with the oracle's quantizer would take some four
     CPU-minutes)."""
     import synth
     from oracle import mxfp4, nvfp4

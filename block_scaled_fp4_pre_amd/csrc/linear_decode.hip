@@ -10,9 +10,9 @@
 // their sums meet in LDS, added in wave order.  The next block's weights are
 // loaded before this block's sums are exchanged.
 //
-// 1 x 4096 x 4096 MXFP4: 4.2 us, 2.1 TB/s with the launch in it (a token kernel and
+// 1 x 4096 x 4096 MXFP4: 4.1 us, 2.2 TB/s with the launch in it (a token kernel and
 // the split kernel: 7.1); 1 x 4096 x 32000: 12.6 us, 5.5 TB/s; 16 x 2048 x 4096 E4M3
-// with addend 6.0.  Quantizing in the lanes that feed the MFMA, each wave its own
+// with addend 5.8.  Quantizing in the lanes that feed the MFMA, each wave its own
 // steps, took 5.8 us for one token: straight code for every step, fetched once
 // and run once, with one token's four lanes of a wave at work.
 #include "linear_common.h"

@@ -17,9 +17,9 @@
 // tile, each with a ring of its own and every other K step, and exchange half of
 // their sums at the end (group 0 finishes the first half of the tokens).
 //
-// 4096 x 4096 x 4096 MXFP4 take 36.0 us (3.8 PFLOP/s), of which about 10 are the
+// 4096 x 4096 x 4096 MXFP4 take 34.9 us (3.9 PFLOP/s), of which about 10 are the
 // first loads and the stores with the matrix cores idle; 16384 x 2048 x 4096 E4M3 120
-// us (2.3), with an addend 141: 134 MB each of outputs and addends at copy speed.
+// us (2.3), with an addend 137: 134 MB each of outputs and addends at copy speed.
 // The steps are bound by power: with 256 x 256 outputs a workgroup a step took as
 // many cycles on 16 CUs as on 256, but the clock fell from 2.26 to 1.75 GHz (MFMAs
 // alone: 2.37 to 1.99).  Such tiles, in 8 waves or in 4 with the accumulators pinned to

@@ -17,7 +17,7 @@
 //
 // Bound by the latency of one token's chain for few tokens (8 x 256, top-6 with a
 // bias: 5.8 us), by instruction issue for many: 16384 x 256 bfloat16 logits, softmax,
-// 12.6 us against 1.8 us for their bytes (13.4 with the chosen logit carried beside its
+// 13.0 us against 1.8 us for their bytes (0.8 more with the chosen logit carried beside its
 // key where there is no bias; 32 with fp64 scores and reductions through LDS).
 #include "device_common.h"
 #include "launch_ops.h"
