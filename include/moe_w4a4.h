@@ -316,7 +316,7 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1, MOE_SCORE_SQRTSOFTPLUS = 2 
 
 /* The router's choice: topk_ids and topk_weights of every forward from the
  * logits of the num_experts experts.  Per token:
- *   s[e]   = score of logit l[e], of the fp64 value rounded to float32;
+ *   s[e]   = score of logit l[e]: its fp64 value rounded to float32;
  *   c[e]   = l[e] when bias is NULL (every scoring rises with the logit), else
  *            s[e] + bias[e] in float32;
  *   groups: experts [j*num_experts/num_groups, ...) are group j; its rank is its
