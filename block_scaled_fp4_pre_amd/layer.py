@@ -235,7 +235,9 @@ class MoeW4A4Layer:
             if isinstance(gate_weight, W4A4Linear):
                 logits = gate_weight.forward(y, dtype=torch.float32)
             else:
-                logits = torch.nn.functional.linear(y, gate_weight)
+                # (autocast may ask for another type, which the router would refuse)
+                with torch.autocast("cuda", enabled=False) if torch.is_autocast_enabled() else contextlib.nullcontext():
+                    logits = torch.nn.functional.linear(y, gate_weight)
             _lib.moe_w4a4_router(logits, ids, weights, bias=bias, scoring=scoring, num_groups=num_groups,
                                  topk_groups=topk_groups, renormalize=renormalize, scale=scale)
             if codes is None:

@@ -246,3 +246,18 @@ def test_block_equals_its_steps(mma, res):
         torch.cuda.synchronize()
         assert out.shape == (n, H) and torch.equal(out, want)
         assert h is x[:n] or torch.equal(h, x[:n] if r is None else ro)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_block_under_autocast(dtype):
+    """torch's own product of the gate keeps its type, whatever autocast asks for."""
+    log(f"[test] block under autocast to {dtype}")
+    layer, shared, _, gate = block(40, MX4)
+    x, r, w, b = (dev_bf16(v) if v.dtype == np.uint16 else dev(v) for v in inputs(40, 13))
+    gd = dev_bf16(gate)
+    want = layer.forward_block(x, r, w, 1e-6, gd, bias=b, shared=shared, **ROUTE)
+    r2 = r.clone()
+    with torch.autocast("cuda", dtype=dtype):
+        got = layer.forward_block(x, r2, w, 1e-6, gd, residual_out=r2, bias=b, shared=shared, **ROUTE)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(r2, want[1])
