@@ -27,6 +27,8 @@ MOE_MEGA_ERR_WORD = 800           # uint64 word of that region that a wait which
 MOE_MEGA_HCOUNT_WORD = 816        # first per-expert h count of that region (words hcount + e)
 
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_SQRTSOFTPLUS = 0, 1, 2
+MOE_FN_NONE, MOE_FN_RELU, MOE_FN_SILU, MOE_FN_GELU, MOE_FN_GELU_TANH = range(5)
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_ROW, MOE_GATE_FULL = range(4)
 
 # Every symbol include/moe_w4a4.h declares.
 EXPORTED = (
@@ -46,6 +48,11 @@ EXPORTED = (
     "moe_w4a4_linear_query",
     "moe_w4a4_linear_prepare",
     "moe_w4a4_linear",
+    "moe_w4a4_linear_bf16",
+    "moe_w4a4_grouped_linear_bf16",
+    "moe_w4a4_experts_bf16_query",
+    "moe_w4a4_experts_bf16",
+    "moe_w4a4_post_norm",
 )
 
 
@@ -62,6 +69,10 @@ class moe_w4a4_cfg(ctypes.Structure):
 
 class moe_w4a4_linear_cfg(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("in_features", "out_features", "max_tokens", "mma_type")]
+
+
+class moe_w4a4_experts_bf16_cfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "num_experts", "topk", "max_tokens", "function")]
 
 
 class moe_w4a4_ws_layout(ctypes.Structure):
@@ -104,6 +115,15 @@ _lib.moe_w4a4_router.argtypes = [_i32, _i32, _i64, _i32, _i32, _i32, _i32, _P, _
 _lib.moe_w4a4_linear_query.argtypes = [_LCFG, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]
 _lib.moe_w4a4_linear_prepare.argtypes = [_LCFG, _P, _P, _P, _sz, _P]
 _lib.moe_w4a4_linear.argtypes = [_LCFG, _P, _i32, _P, _P, _P, _P, _i32, _P, _P, _sz, _P]
+_ECFG = ctypes.POINTER(moe_w4a4_experts_bf16_cfg)
+_lib.moe_w4a4_linear_bf16.argtypes = [_i64, _i32, _i32, _P, _i64, _P, _i32, _i32, _i32, _P, _P, _i32, _P, _i64, _i32,
+                                      _P, _i64, _P]
+_lib.moe_w4a4_grouped_linear_bf16.argtypes = [_i32, _i64, _i32, _i32, _P, _P, _i64, _i64, _P, _i32, _P, _i32, _i32,
+                                              _i32, _P, _P, _i32, _P, _i64, _i32, _P, _i64, _P]
+_lib.moe_w4a4_experts_bf16_query.argtypes = [_ECFG, ctypes.POINTER(_sz)]
+_lib.moe_w4a4_experts_bf16.argtypes = [_ECFG, _P, _P, _i32, _P, _P, _P, _P, _P, _sz, _P]
+_lib.moe_w4a4_post_norm.argtypes = [_i32, _i32, _i32, _i32, _i32, _i64, _i32, _P, _P, _P, _P, _f32, _P, _f32, _f32,
+                                    _P, _P, _P, _P, _P]
 for _n in EXPORTED:
     if _n != "moe_w4a4_status_string":
         getattr(_lib, _n).restype = ctypes.c_int
@@ -483,3 +503,158 @@ def _linear_call(cfg_ref, K: int, N: int, mma_type: int, dev: int, prepared: int
                               workspace, workspace_bytes, _raw_stream(stream, dev))
     if st != MOE_OK:
         raise MoeError(st, "moe_w4a4_linear")
+
+
+# ---- bfloat16 operators around the layer ---------------------------------------
+def _rows_of(t, name: str, dtypes, shape, device_index: int) -> int:
+    """Device address of a matrix whose rows are contiguous and apart (a slice of wider
+    rows, say), as _fits otherwise."""
+    p = _fits(t, name, dtypes, shape, device_index, contiguous=False)
+    # (a size of one may have any stride)
+    if shape[1] > 1 and t.stride(1) != 1 or shape[0] > 1 and t.stride(0) < shape[1]:
+        raise ValueError(f"{name}: strides {t.stride()}, expected rows of {shape[1]} neighbouring values that do not overlap")
+    return p
+
+
+def _row_stride(t) -> int:
+    """Elements from row to row (a single row's stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _product_extras(bias, bias_shape, row_scale, addend, out, dev):
+    """Addresses and codes of what the two products have in common."""
+    T, N = out.shape
+    po = _rows_of(out, "out", _BF16_F32, (T, N), dev)
+    pb = pr = pa = None
+    bias_dtype = add_dtype = lda = 0
+    if bias is not None:
+        pb = _fits(bias, "bias", _BF16_F32, bias_shape, dev)
+        bias_dtype = 1 if bias.dtype is torch.float32 else 0
+    if row_scale is not None:
+        pr = _fits(row_scale, "row_scale", _F32, (T,), dev)
+    if addend is not None:
+        pa = _rows_of(addend, "addend", _BF16_F32, (T, N), dev)
+        add_dtype = 1 if addend.dtype is torch.float32 else 0
+        lda = _row_stride(addend)
+    return bias_dtype, pb, pr, add_dtype, pa, lda, 1 if out.dtype is torch.float32 else 0, po, _row_stride(out)
+
+
+def moe_w4a4_linear_bf16(x, weight, out, bias=None, function: int = MOE_FN_NONE, gated: bool = False, row_scale=None,
+                         addend=None, stream=None) -> None:
+    """out [T, N] (bf16 or float32) = (addend +) (row_scale *) f(x W^T + bias), gated: f(gate)
+    * up.  x bf16 [T, K]; weight bf16 [N, K] (gated: [2N, K], gate rows first); bias bf16 /
+    float32 [N] ([2N]); row_scale float32 [T]; addend bf16 / float32 [T, N] (may be out).
+    The rows of x, addend and out may be slices of wider ones."""
+    dev = _device_of(out, "out")
+    if x.dim() != 2 or out.dim() != 2:
+        raise ValueError(f"x {tuple(x.shape)} and out {tuple(out.shape)}: expected [T, K] and [T, N]")
+    T, K = x.shape[0], x.shape[1]
+    N = out.shape[1]
+    if out.shape[0] != T:
+        raise ValueError(f"out: {out.shape[0]} rows, expected {T}")
+    wide = 2 * N if gated else N
+    px = _rows_of(x, "x", _BF16, (T, K), dev)
+    pw = _fits(weight, "weight", _BF16, (wide, K), dev)
+    bias_dtype, pb, pr, add_dtype, pa, lda, out_dtype, po, ldo = _product_extras(bias, (wide,), row_scale, addend, out, dev)
+    st = _lib.moe_w4a4_linear_bf16(T, K, N, px, _row_stride(x), pw, function, 1 if gated else 0, bias_dtype, pb, pr,
+                                   add_dtype, pa, lda, out_dtype, po, ldo, _raw_stream(stream, dev))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_w4a4_linear_bf16")
+
+
+def moe_w4a4_grouped_linear_bf16(x, weight, offsets, out, rows=None, row_divisor: int = 1, bias=None,
+                                 function: int = MOE_FN_NONE, gated: bool = False, row_scale=None, addend=None,
+                                 stream=None) -> None:
+    """Rows [offsets[e], offsets[e + 1]) of out [R, N] from weight[e], as moe_w4a4_linear_bf16:
+    weight bf16 [E, N, K] (gated: [E, 2N, K]); offsets int32 [E + 1] on the device; bias [E,
+    N] ([E, 2N]).  Row i is x[i], or x[rows[i] // row_divisor] with rows int32 [R]
+    (a forward's sorted_rows and its top-k).  Rows outside the groups stay as they are."""
+    dev = _device_of(out, "out")
+    if x.dim() != 2 or out.dim() != 2 or weight.dim() != 3:
+        raise ValueError(f"x {tuple(x.shape)}, weight {tuple(weight.shape)} and out {tuple(out.shape)}: "
+                         "expected [T, K], [E, N, K] and [R, N]")
+    (Tx, K), (R, N), E = x.shape, out.shape, weight.shape[0]
+    wide = 2 * N if gated else N
+    px = _rows_of(x, "x", _BF16, (Tx, K), dev)
+    pw = _fits(weight, "weight", _BF16, (E, wide, K), dev)
+    pf = _fits(offsets, "offsets", _I32, (E + 1,), dev)
+    pi = None if rows is None else _fits(rows, "rows", _I32, (R,), dev)
+    bias_dtype, pb, pr, add_dtype, pa, lda, out_dtype, po, ldo = _product_extras(bias, (E, wide), row_scale, addend, out,
+                                                                                 dev)
+    st = _lib.moe_w4a4_grouped_linear_bf16(E, R, K, N, pf, px, Tx, _row_stride(x), pi, row_divisor, pw, function,
+                                           1 if gated else 0, bias_dtype, pb, pr, add_dtype, pa, lda, out_dtype, po, ldo,
+                                           _raw_stream(stream, dev))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_w4a4_grouped_linear_bf16")
+
+
+def make_experts_bf16_cfg(hidden: int, inter: int, num_experts: int, topk: int, max_tokens: int,
+                          function: int = MOE_FN_SILU) -> moe_w4a4_experts_bf16_cfg:
+    return moe_w4a4_experts_bf16_cfg(hidden, inter, num_experts, topk, max_tokens, function)
+
+
+def moe_w4a4_experts_bf16_query(cfg: moe_w4a4_experts_bf16_cfg) -> int:
+    """workspace_bytes."""
+    w = _sz()
+    _check(_lib.moe_w4a4_experts_bf16_query(ctypes.byref(cfg), ctypes.byref(w)), "moe_w4a4_experts_bf16_query")
+    return w.value
+
+
+def moe_w4a4_experts_bf16(cfg, w1, w2, x, topk_ids, topk_weights, out, workspace, stream=None) -> None:
+    """out bf16 [T, H] = the routed experts of x bf16 [T, H]: w1 bf16 [E, 2I, H] (gate rows
+    first), w2 bf16 [E, H, I]; topk_ids int32 and topk_weights float32 [T, k]."""
+    dev = _device_of(x, "x")
+    H, I, E, k = cfg.hidden, cfg.inter, cfg.num_experts, cfg.topk
+    T = x.shape[0] if x.dim() == 2 else -1
+    px = _fits(x, "x", _BF16, (T, H), dev)
+    p1 = _fits(w1, "w1", _BF16, (E, 2 * I, H), dev)
+    p2 = _fits(w2, "w2", _BF16, (E, H, I), dev)
+    pi = _fits(topk_ids, "topk_ids", _I32, (T, k), dev)
+    pt = _fits(topk_weights, "topk_weights", _F32, (T, k), dev)
+    po = _fits(out, "out", _BF16, (T, H), dev)
+    pk = _fits(workspace, "workspace", _U8, workspace.shape, dev)
+    _check(_lib.moe_w4a4_experts_bf16(ctypes.byref(cfg), p1, p2, T, px, pi, pt, po, pk, workspace.numel(),
+                                      _raw_stream(stream, dev)), "moe_w4a4_experts_bf16")
+
+
+def moe_w4a4_post_norm(x, residual, residual_out, eps: float, post_weight=None, gate=None, scale: float = 1.0,
+                       next_weight=None, y=None, codes=None, scales=None, mma_type: int = MOE_MMA_MXF4_X_MXF4,
+                       tensor_scale: float = 1.0, stream=None) -> None:
+    """residual_out = residual + scale * gate * z, z the norm of x under post_weight (x itself
+    without one); y, codes and scales = the norm of that under next_weight, as
+    moe_w4a4_add_rmsnorm makes them.  x bf16 [rows, cols]; residual bf16 / float32 [rows, cols]
+    and residual_out like it (may be it); post_weight and next_weight None or [cols], both
+    bf16 or both float32; gate None, or bf16 / float32 of shape [cols], [rows, 1] or [rows, cols];
+    y None or bf16 [rows, cols] (may be x); next_weight is given exactly when y or codes are."""
+    dev = _device_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [rows, cols], got shape {tuple(x.shape)}")
+    rows, cols = shape = x.shape
+    px = _fits(x, "x", _BF16, shape, dev)
+    pr = _fits(residual, "residual", _BF16_F32, shape, dev)
+    pro = _fits(residual_out, "residual_out", (residual.dtype,), shape, dev)
+    p1 = p2 = pg = py = pc = ps = None
+    w_dtype = gate_dtype = 0
+    kind = MOE_GATE_NONE
+    if post_weight is not None:
+        p1 = _fits(post_weight, "post_weight", _BF16_F32, (cols,), dev)
+        w_dtype = 1 if post_weight.dtype is torch.float32 else 0
+    if next_weight is not None:
+        p2 = _fits(next_weight, "next_weight", _BF16_F32 if post_weight is None else (post_weight.dtype,), (cols,), dev)
+        w_dtype = 1 if next_weight.dtype is torch.float32 else 0
+    if gate is not None:
+        kind = MOE_GATE_CHANNEL if gate.dim() == 1 else MOE_GATE_FULL if gate.shape[-1] == cols else MOE_GATE_ROW
+        pg = _fits(gate, "gate", _BF16_F32, ((cols,), (rows, 1), shape)[kind - 1], dev)
+        gate_dtype = 1 if gate.dtype is torch.float32 else 0
+    if y is not None:
+        py = _fits(y, "y", _BF16, shape, dev)
+    if codes is not None or scales is not None:
+        if codes is None or scales is None:
+            raise ValueError("codes and scales go together")
+        pc = _fits(codes, "codes", _U8, (rows, cols if mma_type == MOE_MMA_FP8_X_MXF4 else cols // 2), dev)
+        ps = _fits(scales, "scales", _U8, (rows, cols // (16 if mma_type == MOE_MMA_NVF4_X_NVF4 else 32)), dev)
+    st = _lib.moe_w4a4_post_norm(mma_type, 1 if residual.dtype is torch.float32 else 0, w_dtype, gate_dtype, kind, rows,
+                                 cols, px, pr, p1, pg, scale, p2, eps, tensor_scale, pro, py, pc, ps,
+                                 _raw_stream(stream, dev))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_w4a4_post_norm")

@@ -32,8 +32,8 @@ DEVICE_SOURCES = ("quant.hip", "route.hip", "predispatch.hip", "gemm1.hip", "gem
                   "gemm_nv.hip", "gemm_lds_nv.hip", "combine.hip",
                   "prepare.hip", "noalloc.hip", "mega.hip",
                   "norm.hip", "router.hip", "linear_prepare.hip", "linear.hip", "linear_tile.hip",
-                  "linear_decode.hip")
-HOST_SOURCES = ("abi.cpp", "abi_ops.cpp", "validate.cpp")
+                  "linear_decode.hip", "bf16_split.hip", "post_norm.hip")
+HOST_SOURCES = ("abi.cpp", "abi_ops.cpp", "abi_bf16.cpp", "validate.cpp", "validate_bf16.cpp")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "include")]
 # Packed fp32 VALU ops are kept out of the device code.
 DEVICE_FLAGS = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

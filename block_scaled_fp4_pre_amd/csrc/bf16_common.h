@@ -1,0 +1,171 @@
+// Pieces shared by the kernels of the bfloat16 linears: which rows a workgroup
+// owns, and what happens to a sum on its way out.
+#pragma once
+#include "device_common.h"
+#include "launch_bf16.h"
+#include "moe_w4a4.h"
+#include "pack_bf16.h"
+
+namespace moe {
+
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+// Vectors at the alignment of one element: rows of any N are read and written in
+// whole vectors, which the memory unit takes at any address.
+typedef v2u v2u_at2 __attribute__((aligned(2)));
+typedef v4u v4u_at2 __attribute__((aligned(2)));
+typedef v4f v4f_at4 __attribute__((aligned(4)));
+
+__device__ __forceinline__ v4f mfma_bf16(const v4u& a, const v4u& b, const v4f& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// The rows of a workgroup's tile and their group.
+struct RowTile {
+  int group, first, end;
+};
+
+// Tile number `tile` of the groups' tiles of `size` rows, in the order of the groups.
+// Every wave finds it for itself: a lane counts the tiles of up to 8 consecutive
+// groups, a scan over the lanes says whose it is.  Offsets are clamped to the rows
+// there are, so that wrong ones give wrong rows but no access outside the tensors.
+// False past the last tile.
+__device__ __forceinline__ bool find_tile(const Bf16Args& p, int size, int tile, RowTile& t) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int per = (p.E + kWave - 1) / kWave;
+  int mine = 0;
+  for (int j = 0; j < per; ++j) {
+    const int e = lane * per + j;
+    if (e < p.E) {
+      const int a = min(max(p.offsets[e], 0), p.T), b = min(max(p.offsets[e + 1], 0), p.T);
+      mine += (max(b - a, 0) + size - 1) / size;
+    }
+  }
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int o = __shfl_up(upto, d, kWave);
+    if (lane >= d) upto += o;
+  }
+  const uint64_t past = __ballot(upto > tile);
+  if (past == 0) return false;
+  const int owner = __builtin_ctzll(past);
+  int left = tile - __builtin_amdgcn_readlane(upto - mine, owner);
+  for (int j = 0; j < per; ++j) {
+    const int e = owner * per + j;
+    const int a = min(max(p.offsets[e], 0), p.T), b = min(max(p.offsets[e + 1], 0), p.T);
+    const int n = (max(b - a, 0) + size - 1) / size;
+    if (left < n) {
+      t.group = e;
+      t.first = a + left * size;
+      t.end = min(b, t.first + size);
+      return true;
+    }
+    left -= n;
+  }
+  return false;
+}
+
+// Row of x that row i of the product reads (any index gives a row that exists).
+__device__ __forceinline__ int source_row(const Bf16Args& p, int i) {
+  return p.rows == nullptr ? i : min(max(p.rows[i] / p.row_div, 0), p.x_rows - 1);
+}
+
+// e^v to a few units in the last place: 2^t by the instruction, with the rounding of
+// t = v log2(e) put back (|t| 2^-24 of the result otherwise).
+__device__ __forceinline__ float exp_f32(float v) {
+  v = fminf(fmaxf(v, -104.0f), 89.0f);
+  const float t = v * 1.44269502f;
+  const float r = fmaf(v, 1.92596303e-8f, fmaf(v, 1.44269502f, -t));
+  return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.693147181f, 1.0f);
+}
+
+// f of four sums.  silu(v) = v / (1 + e^-v); gelu = v (1 + erf(v / sqrt 2)) / 2; its
+// tanh form v (1 + tanh u) / 2 = v / (1 + e^-2u), u = sqrt(2/pi) (v + 0.044715 v^3).
+__device__ __forceinline__ v4f apply_function(int fn, v4f v) {
+  switch (fn) {
+    case MOE_FN_RELU:
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
+      break;
+    case MOE_FN_SILU:
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= __builtin_amdgcn_rcpf(1.0f + exp_f32(-v[j]));
+      break;
+    case MOE_FN_GELU:
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= 0.5f * erfcf(v[j] * -0.707106781f);
+      break;
+    case MOE_FN_GELU_TANH:
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] *= __builtin_amdgcn_rcpf(1.0f + exp_f32(v[j] * fmaf(v[j] * v[j], -0.0713548163f, -1.59576912f)));
+      break;
+    default: break;
+  }
+  return v;
+}
+
+__device__ __forceinline__ v4f load4_f32(const void* p, size_t i, bool f32, int left) {
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+  if (f32) {
+    const float* q = static_cast<const float*>(p) + i;
+    if (left >= 4) return *reinterpret_cast<const v4f_at4*>(q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < left) v[j] = q[j];
+  } else {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+    if (left >= 4) {
+      const v2u b = *reinterpret_cast<const v2u_at2*>(q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = bf16_to_f32(b[j / 2] >> (j % 2 * 16) & 0xFFFFu);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < left) v[j] = bf16_to_f32(q[j]);
+    }
+  }
+  return v;
+}
+
+// Four neighbouring outputs of a row from their sums (and, gated, the sums of
+// their up rows): bias, f, row scale and addend in fp32, one rounding.  N - n values
+// of them exist.
+template <bool GATED>
+__device__ __forceinline__ void finish4(const Bf16Args& p, int group, int row, int n, v4f v, const v4f& up) {
+  const int left = p.N - n;
+  if (left <= 0) return;
+  const size_t bias_at = (size_t)group * (GATED ? 2 : 1) * p.N + n;
+  if (p.bias != nullptr) v += load4_f32(p.bias, bias_at, p.bias_f32, left);
+  v = apply_function(p.fn, v);
+  if constexpr (GATED) {
+    v4f u = up;
+    if (p.bias != nullptr) u += load4_f32(p.bias, bias_at + p.N, p.bias_f32, left);
+    v *= u;
+  }
+  if (p.row_scale != nullptr) v *= p.row_scale[row];
+  if (p.addend != nullptr) v += load4_f32(p.addend, (size_t)row * p.lda + n, p.add_f32, left);
+  if (p.out_f32) {
+    float* o = static_cast<float*>(p.out) + (size_t)row * p.ldo + n;
+    if (left >= 4) {
+      *reinterpret_cast<v4f_at4*>(o) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < left) o[j] = v[j];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(p.out) + (size_t)row * p.ldo + n;
+    if (left >= 4) {
+      *reinterpret_cast<v2u_at2*>(o) = v2u{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < left) o[j] = (uint16_t)pack_bf16(v[j], 0.0f);
+    }
+  }
+}
+
+}  // namespace moe

@@ -123,4 +123,37 @@ int check_linear_args(const moe_w4a4_linear_cfg* cfg, const void* prepared, int3
                       const void* xq, const void* xsf, const void* addend, int32_t out_dtype, const void* out,
                       const void* workspace, size_t workspace_bytes, bool* noop);
 
+// ---- bfloat16 operators (validate_bf16.cpp) ----
+constexpr int kBf16MaxK = 65536;
+constexpr int kBf16MaxN = 1 << 20;
+constexpr int64_t kBf16MaxRows = (int64_t)1 << 24;
+constexpr int64_t kBf16MaxOut = (int64_t)1 << 36;      // rows * N: the products' launches stay below 2^32 threads
+constexpr int64_t kBf16MaxStride = (int64_t)1 << 22;   // elements: a tile's rows are within 32-bit byte offsets
+
+// Arguments of moe_w4a4_linear_bf16, moe_w4a4_grouped_linear_bf16 and
+// moe_w4a4_post_norm; *noop: no rows.
+int check_linear_bf16_args(int64_t num_tokens, int32_t K, int32_t N, const void* x, int64_t ldx, const void* w,
+                           int32_t fn, int32_t gated, int32_t bias_dtype, const void* bias, const void* row_scale,
+                           int32_t add_dtype, const void* addend, int64_t lda, int32_t out_dtype, const void* out,
+                           int64_t ldo, bool* noop);
+int check_grouped_bf16_args(int32_t E, int64_t num_rows, int32_t K, int32_t N, const void* offsets, const void* x,
+                            int64_t x_rows, int64_t ldx, const void* rows, int32_t row_divisor, const void* w,
+                            int32_t fn, int32_t gated, int32_t bias_dtype, const void* bias, const void* row_scale,
+                            int32_t add_dtype, const void* addend, int64_t lda, int32_t out_dtype, const void* out,
+                            int64_t ldo, bool* noop);
+int check_post_norm_args(int32_t mma_type, int32_t res_dtype, int32_t w_dtype, int32_t gate_dtype, int32_t gate_kind,
+                         int64_t rows, int32_t cols, const void* x, const void* residual, const void* post_weight,
+                         const void* gate, float scale, const void* next_weight, float eps, float g,
+                         const void* residual_out, const void* y, const void* codes, const void* scales, bool* noop);
+
+// Regions of the workspace of moe_w4a4_experts_bf16 (256-byte aligned).
+struct ExpertsBf16Layout {
+  uint64_t counts, offsets, sorted_rows, pos, hist, h, y, total;
+};
+int check_experts_bf16_cfg(const moe_w4a4_experts_bf16_cfg* c);
+ExpertsBf16Layout experts_bf16_layout(const moe_w4a4_experts_bf16_cfg* c);   // c must pass check_experts_bf16_cfg
+int check_experts_bf16_args(const moe_w4a4_experts_bf16_cfg* cfg, const void* w1, const void* w2, int32_t num_tokens,
+                            const void* x, const void* topk_ids, const void* topk_weights, const void* out,
+                            const void* workspace, size_t workspace_bytes, bool* noop);
+
 }  // namespace moe

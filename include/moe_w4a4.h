@@ -401,6 +401,118 @@ int moe_w4a4_linear(const moe_w4a4_linear_cfg* cfg, const void* prepared, int32_
                     const uint8_t* xq, const uint8_t* xsf, const uint16_t* addend, int32_t out_dtype, void* out,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- bfloat16 operators around the layer -------------------------------- */
+/* What a mixed-precision checkpoint keeps out of the 4-bit formats: router gates,
+ * shared experts, whole expert layers. */
+
+/* function f of a product's sums: none, max(v, 0), v / (1 + exp(-v)), v (1 + erf(v /
+ * sqrt 2)) / 2, and its tanh form v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2. */
+enum { MOE_FN_NONE = 0, MOE_FN_RELU = 1, MOE_FN_SILU = 2, MOE_FN_GELU = 3, MOE_FN_GELU_TANH = 4 };
+
+/* A dense linear with bfloat16 weights:
+ *   v[t, n]   = sum over k of x[t, k] * W[n, k] (+ bias[n])
+ *   out[t, n] = (addend[t, n] +) (row_scale[t] *) f(v[t, n])
+ * gated: W and bias have 2N rows, gate rows [0, N) and up rows [N, 2N) (the order of
+ * the layer's W1), and f(v[t, n]) * v[t, N + n] takes the place of f(v[t, n]).
+ *   x         device bfloat16 [num_tokens, K], 16-byte aligned; row t at x + t *
+ *             x_stride elements (x_stride >= K, a multiple of 8)
+ *   weight    device bfloat16 [N or 2N, K], 16-byte aligned
+ *   bias      NULL, or device [N or 2N] of bias_dtype (0 = bfloat16, 1 = float32)
+ *   row_scale NULL, or device float32 [num_tokens]
+ *   addend    NULL, or device [num_tokens, N] of addend_dtype, addend_stride >= N
+ *             elements from row to row; may be `out` itself where type and stride agree
+ *   out       device [num_tokens, N] of out_dtype, out_stride >= N elements from row to row
+ * K = in_features, N = out_features.  bias, row_scale, addend and out are aligned to their
+ * elements.  out overlaps no input but an addend that it is itself (MOE_EINVAL where it has
+ * the address of one).  Supported: K % 8 == 0, 8 <= K <= 65536, 1 <= N <= 2^20,
+ * num_tokens <= 2^24, num_tokens * N <= 2^36, strides <= 2^22; 0 tokens enqueue nothing
+ * and look at no pointer.  Sums, bias, f, scale and addend are fp32, with one rounding
+ * to out; f is within 2^-20 of its value (an output below 2^-126 within 2^-126).  The
+ * order of a sum is fixed by the sizes: the result is deterministic, sums of another
+ * num_tokens may be ordered otherwise.  A row's non-finite values stay in its outputs.
+ * No workspace: calls may run at the same time. */
+int moe_w4a4_linear_bf16(int64_t num_tokens, int32_t in_features, int32_t out_features, const uint16_t* x,
+                         int64_t x_stride, const uint16_t* weight, int32_t function, int32_t gated, int32_t bias_dtype,
+                         const void* bias, const float* row_scale, int32_t addend_dtype, const void* addend,
+                         int64_t addend_stride, int32_t out_dtype, void* out, int64_t out_stride, void* stream);
+
+/* The same for rows sorted by group (expert): rows [offsets[e], offsets[e + 1]) are
+ * multiplied by W[e] and take bias[e].
+ *   offsets  device int32 [num_groups + 1], rising, within [0, num_rows]; groups may be
+ *            empty.  Rows of out outside [offsets[0], offsets[num_groups]) stay as they
+ *            are.  The library cannot read them on the host: wrong offsets give
+ *            unspecified numbers, never an access outside the tensors
+ *   rows     NULL (row i is x[i], x_rows >= num_rows), or device int32 [num_rows]: row i is
+ *            x[rows[i] / row_divisor].  A forward's sorted_rows with row_divisor = topk
+ *            are such (an index outside x gives unspecified numbers).  With rows, x_rows
+ *            * x_stride < 2^31
+ *   weight   device bfloat16 [num_groups, N or 2N, K]; bias [num_groups, N or 2N]
+ *   row_scale, addend and out have num_rows rows.
+ * 1 <= num_groups <= 512; the rest as for moe_w4a4_linear_bf16. */
+int moe_w4a4_grouped_linear_bf16(int32_t num_groups, int64_t num_rows, int32_t in_features, int32_t out_features,
+                                 const int32_t* offsets, const uint16_t* x, int64_t x_rows, int64_t x_stride,
+                                 const int32_t* rows, int32_t row_divisor, const uint16_t* weight, int32_t function,
+                                 int32_t gated, int32_t bias_dtype, const void* bias, const float* row_scale,
+                                 int32_t addend_dtype, const void* addend, int64_t addend_stride, int32_t out_dtype,
+                                 void* out, int64_t out_stride, void* stream);
+
+/* Routed experts with bfloat16 weights, for expert layers left unquantized: the steps
+ * of moe_w4a4_forward without its quantization.  Supported: hidden and inter multiples
+ * of 8 up to 65536, 1 <= num_experts <= 512, 1 <= topk <= 16, max_tokens * topk <= 2^24,
+ * max_tokens * hidden < 2^31. */
+typedef struct moe_w4a4_experts_bf16_cfg {
+  int32_t hidden;       /* H */
+  int32_t inter;        /* I */
+  int32_t num_experts;  /* E */
+  int32_t topk;         /* k */
+  int32_t max_tokens;   /* capacity of the workspace */
+  int32_t function;     /* MOE_FN_*: h = f(gate) * up (MOE_FN_SILU: SwiGLU) */
+} moe_w4a4_experts_bf16_cfg;
+
+int moe_w4a4_experts_bf16_query(const moe_w4a4_experts_bf16_cfg* cfg, size_t* workspace_bytes);
+
+/* w1 device bfloat16 [E, 2I, H] (rows [0, I) gate, [I, 2I) up), w2 [E, H, I], both
+ * 16-byte aligned.  h and the second products are rounded to bfloat16; out[t] = sum over
+ * valid slots j, in slot order, of topk_weights[t, j] * y[row (t, j)] in fp32, rounded to
+ * bfloat16.  x, topk_ids, topk_weights, out, num_tokens and errors as for moe_w4a4_forward
+ * (out may be x); workspace: device buffer of query's workspace_bytes, 256-byte
+ * aligned, any contents at the start; calls that share one must not overlap. */
+int moe_w4a4_experts_bf16(const moe_w4a4_experts_bf16_cfg* cfg, const uint16_t* w1, const uint16_t* w2,
+                          int32_t num_tokens, const uint16_t* x, const int32_t* topk_ids, const float* topk_weights,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* gate_kind: what `gate` of moe_w4a4_post_norm holds: nothing, a value for each column
+ * ([cols]), for each row ([rows]) or for each element ([rows, cols]). */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_ROW = 2, MOE_GATE_FULL = 3 };
+
+/* The norm after a block with its gate and residual scale, the addition to the
+ * residual stream, and the norm and quantization before the next block:
+ *   z = x                                        without a post_weight (NULL), else
+ *   z = x * post_weight / sqrt(mean(x^2 along the row) + eps)
+ *   h = residual + scale * gate * z              rounded to float32, then (bfloat16 streams) to bfloat16
+ *   y, codes, scales = the norm of h under next_weight and what moe_w4a4_add_rmsnorm
+ *                      makes of it, with the same eps.
+ * Both sums, the norms and every product are fp64, as there.
+ *   x            device bfloat16 [rows, cols]: a block's output
+ *   residual     device [rows, cols] of res_dtype (0 = bfloat16, 1 = float32)
+ *   post_weight  NULL, or device [cols] of w_dtype (0 = bfloat16, 1 = float32)
+ *   gate         device values of gate_dtype (0, 1) as gate_kind says, NULL exactly for MOE_GATE_NONE
+ *   next_weight  device [cols] of w_dtype; NULL exactly when y and codes both are (h alone)
+ *   residual_out device [rows, cols] of res_dtype: h; may be `residual` itself (or x, if
+ *                that has its type)
+ *   y            NULL, or device bfloat16 [rows, cols]; may be x itself, or `residual` if
+ *                that is bfloat16 and not residual_out
+ *   codes, scales, mma_type, g   as for moe_w4a4_add_rmsnorm
+ * All tensors 16-byte aligned but scales and a gate of rows; no other overlap of inputs and
+ * outputs than those named (MOE_EINVAL where an output has the address of another,
+ * or of an input that it may not be).  cols % 32 == 0, cols <= 65536, rows >= 0 (0
+ * enqueues nothing and looks at no pointer), eps finite and > 0, scale finite.  Values
+ * must be finite, as there: a row with others leaves the other rows alone. */
+int moe_w4a4_post_norm(int32_t mma_type, int32_t res_dtype, int32_t w_dtype, int32_t gate_dtype, int32_t gate_kind,
+                       int64_t rows, int32_t cols, const uint16_t* x, const void* residual, const void* post_weight,
+                       const void* gate, float scale, const void* next_weight, float eps, float g, void* residual_out,
+                       uint16_t* y, uint8_t* codes, uint8_t* scales, void* stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* moe_w4a4_status_string(int status);
 
