@@ -25,14 +25,15 @@ PROBE_SOURCES = ("ceiling.hip",)
 # The MFMA probe and the linear's tile kernel keep their accumulators in VGPRs:
 # in AGPRs the compiler rotated them through copies on every loop iteration.
 SOURCE_FLAGS = {"ceiling.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-                "linear_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+                "linear_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+                "bf16_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 ARCH = "gfx950"
 
 DEVICE_SOURCES = ("quant.hip", "route.hip", "predispatch.hip", "gemm1.hip", "gemm2.hip", "gemm_lds.hip",
                   "gemm_nv.hip", "gemm_lds_nv.hip", "combine.hip",
                   "prepare.hip", "noalloc.hip", "mega.hip",
                   "norm.hip", "router.hip", "linear_prepare.hip", "linear.hip", "linear_tile.hip",
-                  "linear_decode.hip", "bf16_split.hip", "post_norm.hip")
+                  "linear_decode.hip", "bf16_split.hip", "bf16_tile.hip", "post_norm.hip")
 HOST_SOURCES = ("abi.cpp", "abi_ops.cpp", "abi_bf16.cpp", "validate.cpp", "validate_bf16.cpp")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "include")]
 # Packed fp32 VALU ops are kept out of the device code.

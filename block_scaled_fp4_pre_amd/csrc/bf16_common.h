@@ -26,46 +26,48 @@ struct RowTile {
   int group, first, end;
 };
 
-// Tile number `tile` of the groups' tiles of `size` rows, in the order of the groups.
-// Every wave finds it for itself: a lane counts the tiles of up to 8 consecutive
-// groups, a scan over the lanes says whose it is.  Offsets are clamped to the rows
-// there are, so that wrong ones give wrong rows but no access outside the tensors.
-// False past the last tile.
-__device__ __forceinline__ bool find_tile(const Bf16Args& p, int size, int tile, RowTile& t) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int per = (p.E + kWave - 1) / kWave;
-  int mine = 0;
-  for (int j = 0; j < per; ++j) {
-    const int e = lane * per + j;
-    if (e < p.E) {
-      const int a = min(max(p.offsets[e], 0), p.T), b = min(max(p.offsets[e + 1], 0), p.T);
-      mine += (max(b - a, 0) + size - 1) / size;
-    }
-  }
-  int upto = mine;
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int o = __shfl_up(upto, d, kWave);
-    if (lane >= d) upto += o;
-  }
-  const uint64_t past = __ballot(upto > tile);
-  if (past == 0) return false;
-  const int owner = __builtin_ctzll(past);
-  int left = tile - __builtin_amdgcn_readlane(upto - mine, owner);
-  for (int j = 0; j < per; ++j) {
-    const int e = owner * per + j;
+// The groups' tiles of `size` rows, in the order of the groups.  Every wave counts them
+// for itself: a lane those of up to 8 consecutive groups, a scan over the lanes says
+// whose a tile is.  Offsets are clamped to the rows there are, so that wrong ones
+// give wrong rows but no access outside the tensors.
+struct GroupTiles {
+  int per, mine, upto, total;
+  __device__ __forceinline__ static int2 rows(const Bf16Args& p, int e) {
     const int a = min(max(p.offsets[e], 0), p.T), b = min(max(p.offsets[e + 1], 0), p.T);
-    const int n = (max(b - a, 0) + size - 1) / size;
-    if (left < n) {
-      t.group = e;
-      t.first = a + left * size;
-      t.end = min(b, t.first + size);
-      return true;
-    }
-    left -= n;
+    return make_int2(a, max(a, b));
   }
-  return false;
-}
+  __device__ __forceinline__ GroupTiles(const Bf16Args& p, int size) {
+    const int lane = threadIdx.x & (kWave - 1);
+    per = (p.E + kWave - 1) / kWave;
+    mine = 0;
+    for (int j = 0; j < per; ++j) {
+      const int e = lane * per + j;
+      if (e < p.E) {
+        const int2 r = rows(p, e);
+        mine += (r.y - r.x + size - 1) / size;
+      }
+    }
+    upto = mine;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int o = __shfl_up(upto, d, kWave);
+      if (lane >= d) upto += o;
+    }
+    total = __builtin_amdgcn_readlane(upto, kWave - 1);
+  }
+  // Tile number `tile` < total.
+  __device__ __forceinline__ RowTile find(const Bf16Args& p, int size, int tile) const {
+    const int owner = __builtin_ctzll(__ballot(upto > tile));
+    int left = tile - __builtin_amdgcn_readlane(upto - mine, owner), e = owner * per;
+    for (;; ++e) {
+      const int2 r = rows(p, e);
+      const int n = (r.y - r.x + size - 1) / size;
+      if (left < n) return {e, r.x + left * size, min(r.y, r.x + (left + 1) * size)};
+      left -= n;
+      if (e + 1 >= p.E) return {e, 0, 1};     // (offsets that changed under the kernel)
+    }
+  }
+};
 
 // Row of x that row i of the product reads (any index gives a row that exists).
 __device__ __forceinline__ int source_row(const Bf16Args& p, int i) {

@@ -26,16 +26,20 @@ template <int NT, int NR, bool GATED, bool GROUPED>
 __global__ void __launch_bounds__(64 * kSplitWaves) bf16_split_kernel(Bf16Args p, int row_tiles, int tok_tiles) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int COLS = GATED ? NR * 8 : NR * 16;     // outputs a row
-  // Workgroups are dealt round-robin to the 8 XCDs: each XCD gets a run of the order below.
-  const int L = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
-  if (L >= row_tiles * tok_tiles) return;
+  // Workgroups are dealt round-robin to the 8 XCDs: each XCD gets a run of the order
+  // below, a group's or token tile's rows of the weights next to each other.
   int rt, tt;
   RowTile t;
   if constexpr (GROUPED) {
+    const GroupTiles tiles(p, NT * 16);
+    const int per = (tiles.total * row_tiles + 7) / 8, at = blockIdx.x >> 3, L = (blockIdx.x & 7) * per + at;
+    if (at >= per || L >= tiles.total * row_tiles) return;
     tt = L / row_tiles;
     rt = L - tt * row_tiles;
-    if (!find_tile(p, NT * 16, tt, t)) return;
+    t = tiles.find(p, NT * 16, tt);
   } else {
+    const int L = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    if (L >= row_tiles * tok_tiles) return;
     rt = L / tok_tiles;
     tt = L - rt * tok_tiles;
     t = {0, tt * NT * 16, min(p.T, (tt + 1) * NT * 16)};
@@ -164,7 +168,7 @@ hipError_t launch_rows(const Bf16Args& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_linear_bf16(bool gated, const Bf16Args& a, hipStream_t stream) {
+hipError_t launch_bf16_split(bool gated, const Bf16Args& a, hipStream_t stream) {
   if (a.offsets != nullptr) return gated ? launch_rows<true, true>(a, stream) : launch_rows<false, true>(a, stream);
   return gated ? launch_rows<true, false>(a, stream) : launch_rows<false, false>(a, stream);
 }

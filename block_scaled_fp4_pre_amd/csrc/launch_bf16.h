@@ -25,7 +25,12 @@ struct Bf16Args {
   bool bias_f32, add_f32, out_f32;
 };
 
-hipError_t launch_linear_bf16(bool gated, const Bf16Args& a, hipStream_t stream);
+hipError_t launch_bf16_split(bool gated, const Bf16Args& a, hipStream_t stream);   // bf16_split.hip
+hipError_t launch_bf16_tile(bool gated, const Bf16Args& a, hipStream_t stream);    // bf16_tile.hip
+inline hipError_t launch_linear_bf16(bool gated, const Bf16Args& a, hipStream_t stream) {
+  const int64_t rows = a.offsets != nullptr ? (a.T + a.E - 1) / a.E : a.T;
+  return rows > 64 ? launch_bf16_tile(gated, a, stream) : launch_bf16_split(gated, a, stream);
+}
 
 // post_norm.hip.  act as for launch_add_rmsnorm; gate_kind: MOE_GATE_*.
 struct PostNormArgs {

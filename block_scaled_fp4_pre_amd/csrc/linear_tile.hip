@@ -27,23 +27,10 @@
 // 143 for E4M3 16384 x 2048 x 4096; reading the next step's operands into registers
 // during a step changed nothing at two workgroups a CU.
 #include "linear_common.h"
+#include "tile_dma.h"
 
 namespace moe {
 namespace {
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// The 16 (4) bytes at base + voff of lane l go to LDS byte address lds + 16*l
-// (4*l); base and lds are the wave's own (scalar).  M0 carries the LDS address; a
-// DMA right after a scalar write of M0 needs one wait state, which the compiler
-// cannot insert inside an asm statement.
-__device__ __forceinline__ void dma16(const uint8_t* base, int voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(const uint8_t* base, int voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 constexpr int kTileWaves = 4;   // of a group
 constexpr int kTileBand = 8;    // row tiles
@@ -63,18 +50,6 @@ struct TileShape {
   static_assert(AD * WAVES == AB && BD * WAVES == BB * (TB / 1024) && AB % 4 == 0 && BB % 4 == 0, "DMA shares");
   static_assert(WA % 4 == 0 && (WB % 4 == 0 || WB == 2), "scale dwords");
 };
-
-template <int N>
-struct Int {
-  static constexpr int value = N;
-};
-template <int N, int I = 0, class F>
-__device__ __forceinline__ void unrolled(F&& f) {
-  if constexpr (I < N) {
-    f(Int<I>{});
-    unrolled<N, I + 1>(f);
-  }
-}
 
 // The wave's outputs acc[token block][row block] to rows t0.. and columns n0..
 // of `out`, G token blocks at a time through `mine` (G*16 x STRIDE bytes of

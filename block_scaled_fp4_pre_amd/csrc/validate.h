@@ -128,6 +128,7 @@ constexpr int kBf16MaxK = 65536;
 constexpr int kBf16MaxN = 1 << 20;
 constexpr int64_t kBf16MaxRows = (int64_t)1 << 24;
 constexpr int64_t kBf16MaxOut = (int64_t)1 << 36;      // rows * N: the products' launches stay below 2^32 threads
+constexpr int64_t kBf16MaxGroupCols = (int64_t)1 << 24;  // groups * N: the same
 constexpr int64_t kBf16MaxStride = (int64_t)1 << 22;   // elements: a tile's rows are within 32-bit byte offsets
 
 // Arguments of moe_w4a4_linear_bf16, moe_w4a4_grouped_linear_bf16 and

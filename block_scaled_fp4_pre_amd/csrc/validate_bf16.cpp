@@ -60,7 +60,7 @@ int check_grouped_bf16_args(int32_t E, int64_t num_rows, int32_t K, int32_t N, c
                             int64_t ldo, bool* noop) {
   *noop = false;
   if (E <= 0 || row_divisor <= 0) return MOE_EINVAL;
-  if (E > kMaxExperts) return MOE_EUNSUPPORTED;
+  if (E > kMaxExperts || (int64_t)E * N > kBf16MaxGroupCols) return MOE_EUNSUPPORTED;
   const int st = check_product(num_rows, x_rows, K, N, x, ldx, w, fn, gated, bias_dtype, bias, row_scale, add_dtype,
                                addend, lda, out_dtype, out, ldo, noop);
   if (st != MOE_OK || *noop) return st;
@@ -77,7 +77,9 @@ int check_experts_bf16_cfg(const moe_w4a4_experts_bf16_cfg* c) {
   if (c->hidden <= 0 || c->inter <= 0 || c->num_experts <= 0 || c->topk <= 0 || c->max_tokens < 0) return MOE_EINVAL;
   if (c->hidden % 8 != 0 || c->inter % 8 != 0 || c->hidden > kBf16MaxK || c->inter > kBf16MaxK ||
       c->num_experts > kMaxExperts || c->topk > kMaxTopk || (int64_t)c->max_tokens * c->topk > kBf16MaxRows ||
-      (int64_t)c->max_tokens * c->hidden >= (int64_t)1 << 31)
+      (int64_t)c->max_tokens * c->hidden >= (int64_t)1 << 31 ||
+      (int64_t)c->num_experts * c->inter > kBf16MaxGroupCols || (int64_t)c->num_experts * c->hidden > kBf16MaxGroupCols ||
+      (int64_t)c->max_tokens * c->topk * c->hidden > kBf16MaxOut || (int64_t)c->max_tokens * c->topk * c->inter > kBf16MaxOut)
     return MOE_EUNSUPPORTED;
   if (c->function < MOE_FN_NONE || c->function > MOE_FN_GELU_TANH) return MOE_EUNSUPPORTED;
   return MOE_OK;

@@ -448,7 +448,7 @@ int moe_w4a4_linear_bf16(int64_t num_tokens, int32_t in_features, int32_t out_fe
  *            * x_stride < 2^31
  *   weight   device bfloat16 [num_groups, N or 2N, K]; bias [num_groups, N or 2N]
  *   row_scale, addend and out have num_rows rows.
- * 1 <= num_groups <= 512; the rest as for moe_w4a4_linear_bf16. */
+ * 1 <= num_groups <= 512, num_groups * N <= 2^24; the rest as for moe_w4a4_linear_bf16. */
 int moe_w4a4_grouped_linear_bf16(int32_t num_groups, int64_t num_rows, int32_t in_features, int32_t out_features,
                                  const int32_t* offsets, const uint16_t* x, int64_t x_rows, int64_t x_stride,
                                  const int32_t* rows, int32_t row_divisor, const uint16_t* weight, int32_t function,
@@ -458,8 +458,8 @@ int moe_w4a4_grouped_linear_bf16(int32_t num_groups, int64_t num_rows, int32_t i
 
 /* Routed experts with bfloat16 weights, for expert layers left unquantized: the steps
  * of moe_w4a4_forward without its quantization.  Supported: hidden and inter multiples
- * of 8 up to 65536, 1 <= num_experts <= 512, 1 <= topk <= 16, max_tokens * topk <= 2^24,
- * max_tokens * hidden < 2^31. */
+ * of 8 up to 65536, 1 <= num_experts <= 512, num_experts times either <= 2^24, 1 <= topk <=
+ * 16, max_tokens * topk <= 2^24 and times either <= 2^36, max_tokens * hidden < 2^31. */
 typedef struct moe_w4a4_experts_bf16_cfg {
   int32_t hidden;       /* H */
   int32_t inter;        /* I */
