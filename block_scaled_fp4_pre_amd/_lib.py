@@ -28,6 +28,7 @@ MOE_MEGA_HCOUNT_WORD = 816        # first per-expert h count of that region (wor
 
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_SQRTSOFTPLUS = 0, 1, 2
 MOE_FN_NONE, MOE_FN_RELU, MOE_FN_SILU, MOE_FN_GELU, MOE_FN_GELU_TANH = range(5)
+MOE_BF16_MAX_ROWS = 1 << 24      # tokens that the bfloat16 products take
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_ROW, MOE_GATE_FULL = range(4)
 
 # Every symbol include/moe_w4a4.h declares.
@@ -562,6 +563,13 @@ def moe_w4a4_linear_bf16(x, weight, out, bias=None, function: int = MOE_FN_NONE,
         raise MoeError(st, "moe_w4a4_linear_bf16")
 
 
+def _check_linear_bf16_config(in_features: int, out_features: int, function: int) -> None:
+    """Raise what moe_w4a4_linear_bf16 would raise for its plain arguments (the library
+    checks them for no tokens too)."""
+    _check(_lib.moe_w4a4_linear_bf16(0, in_features, out_features, None, in_features, None, function, 0, 0, None, None, 0,
+                                     None, 0, 0, None, out_features, None), "moe_w4a4_linear_bf16")
+
+
 def moe_w4a4_grouped_linear_bf16(x, weight, offsets, out, rows=None, row_divisor: int = 1, bias=None,
                                  function: int = MOE_FN_NONE, gated: bool = False, row_scale=None, addend=None,
                                  stream=None) -> None:
@@ -617,6 +625,11 @@ def moe_w4a4_experts_bf16(cfg, w1, w2, x, topk_ids, topk_weights, out, workspace
                                       _raw_stream(stream, dev)), "moe_w4a4_experts_bf16")
 
 
+def _gate_kind(gate, rows: int, cols: int) -> int:
+    """MOE_GATE_* of a gate by its shape: [cols], [rows, 1] or [rows, cols]."""
+    return MOE_GATE_CHANNEL if gate.dim() == 1 else MOE_GATE_ROW if gate.shape[-1] == 1 else MOE_GATE_FULL
+
+
 def moe_w4a4_post_norm(x, residual, residual_out, eps: float, post_weight=None, gate=None, scale: float = 1.0,
                        next_weight=None, y=None, codes=None, scales=None, mma_type: int = MOE_MMA_MXF4_X_MXF4,
                        tensor_scale: float = 1.0, stream=None) -> None:
@@ -643,7 +656,7 @@ def moe_w4a4_post_norm(x, residual, residual_out, eps: float, post_weight=None, 
         p2 = _fits(next_weight, "next_weight", _BF16_F32 if post_weight is None else (post_weight.dtype,), (cols,), dev)
         w_dtype = 1 if next_weight.dtype is torch.float32 else 0
     if gate is not None:
-        kind = MOE_GATE_CHANNEL if gate.dim() == 1 else MOE_GATE_FULL if gate.shape[-1] == cols else MOE_GATE_ROW
+        kind = _gate_kind(gate, rows, cols)
         pg = _fits(gate, "gate", _BF16_F32, ((cols,), (rows, 1), shape)[kind - 1], dev)
         gate_dtype = 1 if gate.dtype is torch.float32 else 0
     if y is not None:

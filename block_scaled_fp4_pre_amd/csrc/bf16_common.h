@@ -15,6 +15,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 // whole vectors, which the memory unit takes at any address.
 typedef v2u v2u_at2 __attribute__((aligned(2)));
 typedef v4u v4u_at2 __attribute__((aligned(2)));
+typedef v4u v4u_at4 __attribute__((aligned(4)));
 typedef v4f v4f_at4 __attribute__((aligned(4)));
 
 __device__ __forceinline__ v4f mfma_bf16(const v4u& a, const v4u& b, const v4f& c) {
@@ -74,17 +75,46 @@ __device__ __forceinline__ int source_row(const Bf16Args& p, int i) {
   return p.rows == nullptr ? i : min(max(p.rows[i] / p.row_div, 0), p.x_rows - 1);
 }
 
-// e^v to a few units in the last place: 2^t by the instruction, with the rounding of
-// t = v log2(e) put back (|t| 2^-24 of the result otherwise).
-__device__ __forceinline__ float exp_f32(float v) {
-  v = fminf(fmaxf(v, -104.0f), 89.0f);
-  const float t = v * 1.44269502f;
-  const float r = fmaf(v, 1.92596303e-8f, fmaf(v, 1.44269502f, -t));
-  return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.693147181f, 1.0f);
+// v / (1 + 2^(t + r)), r the rounding of t (left out it would cost |t| 2^-24 of a small
+// result).  Far out 2^t is taken 2^32 times smaller and 1 is nothing next to it: the
+// reciprocal of a power past 2^126 would be flushed to zero where v / 2^t is not.
+// (Contraction is off where a product's rounding is known and put back: fused into a later
+// sum the product would have another.)
+__device__ __forceinline__ float over_one_plus_exp2(float v, float t, float r) {
+#pragma clang fp contract(off)
+  const bool far = t > 64.0f;
+  const float e = __builtin_amdgcn_exp2f(far ? t - 32.0f : t) * fmaf(r, 0.693147181f, 1.0f);
+  const float q = v * __builtin_amdgcn_rcpf(far ? e : 1.0f + e);
+  return far ? q * 0x1p-32f : q;
 }
 
-// f of four sums.  silu(v) = v / (1 + e^-v); gelu = v (1 + erf(v / sqrt 2)) / 2; its
-// tanh form v (1 + tanh u) / 2 = v / (1 + e^-2u), u = sqrt(2/pi) (v + 0.044715 v^3).
+// silu(v) = v / (1 + e^-v).
+__device__ __forceinline__ float silu_f32(float v) {
+#pragma clang fp contract(off)
+  const float u = fminf(fmaxf(-v, -104.0f), 200.0f), t = u * 1.44269502f;
+  return over_one_plus_exp2(v, t, fmaf(u, 1.92596303e-8f, fmaf(u, 1.44269502f, -t)));
+}
+
+// gelu(v) = v erfc(-v / sqrt 2) / 2, the rounding of erfc's argument put back: erfc(x + d) =
+// erfc(x) (1 - h d), h = 2 e^(-x^2) / (sqrt(pi) erfc(x)), which lies between x + sqrt(x^2 + 4/pi)
+// and x + sqrt(x^2 + 2) for x > 0 (and is nothing next to 1 / x below -4).
+__device__ __forceinline__ float gelu_f32(float v) {
+#pragma clang fp contract(off)
+  const float x = v * -0.707106769f, d = fmaf(v, -1.21016175e-8f, fmaf(v, -0.707106769f, -x));
+  const float y = fminf(x, 16.0f), h = y + __builtin_amdgcn_sqrtf(fmaf(y, y, 1.4f));
+  return v * (0.5f * erfcf(x)) * (x < -4.0f ? 1.0f : fmaf(-h, d, 1.0f));
+}
+
+// Its tanh form: v (1 + tanh u) / 2 = v / (1 + e^-2u), u = sqrt(2/pi) (v + 0.044715 v^3); the
+// exponent in fp64, for a cubic's roundings would be as large as a small result's bits.
+__device__ __forceinline__ float gelu_tanh_f32(float v) {
+  const double w = v;
+  const double t = fmin(fmax(w * fma(w * w, -0.1029432395800235, -2.302208198144325), -150.0), 300.0);
+  const float high = (float)t;
+  return over_one_plus_exp2(v, high, (float)(t - (double)high));
+}
+
+// f of four sums.
 __device__ __forceinline__ v4f apply_function(int fn, v4f v) {
   switch (fn) {
     case MOE_FN_RELU:
@@ -93,16 +123,15 @@ __device__ __forceinline__ v4f apply_function(int fn, v4f v) {
       break;
     case MOE_FN_SILU:
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] *= __builtin_amdgcn_rcpf(1.0f + exp_f32(-v[j]));
+      for (int j = 0; j < 4; ++j) v[j] = silu_f32(v[j]);
       break;
     case MOE_FN_GELU:
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] *= 0.5f * erfcf(v[j] * -0.707106781f);
+      for (int j = 0; j < 4; ++j) v[j] = gelu_f32(v[j]);
       break;
     case MOE_FN_GELU_TANH:
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] *= __builtin_amdgcn_rcpf(1.0f + exp_f32(v[j] * fmaf(v[j] * v[j], -0.0713548163f, -1.59576912f)));
+      for (int j = 0; j < 4; ++j) v[j] = gelu_tanh_f32(v[j]);
       break;
     default: break;
   }
