@@ -22,22 +22,31 @@ __device__ __forceinline__ v4f mfma_bf16(const v4u& a, const v4u& b, const v4f& 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// The rows of a workgroup's tile and their group.
+// A group and its rows; the rows of its tiles, which of them, of how many.
 struct RowTile {
-  int group, first, end;
+  int group, first, end, size, tile, tiles;
 };
 
-// The groups' tiles of `size` rows, in the order of the groups.  Every wave counts them
-// for itself: a lane those of up to 8 consecutive groups, a scan over the lanes says
-// whose a tile is.  Offsets are clamped to the rows there are, so that wrong ones
-// give wrong rows but no access outside the tensors.
+// Rows a tile of a group of n rows has, in units of UNIT: as few tiles as `cap` units each
+// allow, all of them as even as the units are.
+template <int UNIT>
+__host__ __device__ __forceinline__ int tile_rows(int n, int cap) {
+  const int tiles = (n + UNIT * cap - 1) / (UNIT * cap);
+  return tiles <= 1 ? UNIT * cap : (n + UNIT * tiles - 1) / (UNIT * tiles) * UNIT;
+}
+
+// The groups' tiles, in the order of the groups.  Every wave counts them for itself: a
+// lane those of up to 8 consecutive groups, a scan over the lanes says whose a tile is.
+// Offsets are clamped to the rows there are, so that wrong ones give wrong rows but no
+// access outside the tensors.
+template <int UNIT>
 struct GroupTiles {
-  int per, mine, upto, total;
+  int cap, per, mine, upto, total;
   __device__ __forceinline__ static int2 rows(const Bf16Args& p, int e) {
     const int a = min(max(p.offsets[e], 0), p.T), b = min(max(p.offsets[e + 1], 0), p.T);
     return make_int2(a, max(a, b));
   }
-  __device__ __forceinline__ GroupTiles(const Bf16Args& p, int size) {
+  __device__ __forceinline__ GroupTiles(const Bf16Args& p, int units) : cap(units) {
     const int lane = threadIdx.x & (kWave - 1);
     per = (p.E + kWave - 1) / kWave;
     mine = 0;
@@ -45,6 +54,7 @@ struct GroupTiles {
       const int e = lane * per + j;
       if (e < p.E) {
         const int2 r = rows(p, e);
+        const int size = tile_rows<UNIT>(r.y - r.x, cap);
         mine += (r.y - r.x + size - 1) / size;
       }
     }
@@ -56,19 +66,32 @@ struct GroupTiles {
     }
     total = __builtin_amdgcn_readlane(upto, kWave - 1);
   }
-  // Tile number `tile` < total.
-  __device__ __forceinline__ RowTile find(const Bf16Args& p, int size, int tile) const {
+  // Tile number `tile` < total: its group, the group's rows and tiles, and which of them it is.
+  __device__ __forceinline__ RowTile find(const Bf16Args& p, int tile) const {
     const int owner = __builtin_ctzll(__ballot(upto > tile));
     int left = tile - __builtin_amdgcn_readlane(upto - mine, owner), e = owner * per;
     for (;; ++e) {
       const int2 r = rows(p, e);
+      const int size = tile_rows<UNIT>(r.y - r.x, cap);
       const int n = (r.y - r.x + size - 1) / size;
-      if (left < n) return {e, r.x + left * size, min(r.y, r.x + (left + 1) * size)};
+      if (left < n) return {e, r.x, r.y, size, left, n};
       left -= n;
-      if (e + 1 >= p.E) return {e, 0, 1};     // (offsets that changed under the kernel)
+      if (e + 1 >= p.E) return {e, 0, 1, UNIT * cap, 0, 1};     // (offsets that changed under the kernel)
     }
   }
 };
+
+// The place of a workgroup among `total` items of the groups, or -1.  Workgroups are
+// dealt round-robin to the 8 XCDs; each XCD takes runs of 32 items in turn, as many as it
+// has CUs, so that items next to each other share operands in its L2 and groups of
+// unlike size spread over the XCDs.
+constexpr int kRun = 32;
+__device__ __forceinline__ int group_item(int total) {
+  const int at = blockIdx.x >> 3, L = (at / kRun * 8 + (blockIdx.x & 7)) * kRun + at % kRun;
+  return L < total ? L : -1;
+}
+// Workgroups that cover `total` items so.
+inline int64_t group_grid(int64_t total) { return (total + 8 * kRun - 1) / (8 * kRun) * (8 * kRun); }
 
 // Row of x that row i of the product reads (any index gives a row that exists).
 __device__ __forceinline__ int source_row(const Bf16Args& p, int i) {

@@ -6,156 +6,55 @@
 // operand read spread over the banks (a copy fills places in order: the lane picks the
 // piece instead).
 //
-// Two stages, and the operand registers of half a stage read ahead: a step's first half
-// multiplies k 0..31 while it reads k 32..63; then one barrier says that the next stage has
-// landed and that this one was read; the second half multiplies k 32..63 while it reads
-// the next stage's first operands and copies the stage after that into this one's place.
-// Every copy has a whole step to land, and the matrix cores do not wait for LDS at a
-// step's start.  The copies are inline assembly (tile_dma.h): the compiler cannot tell the
+// A ring of P stages, and the operand registers of half a stage read ahead: a step's first
+// half multiplies k 0..31 while it reads k 32..63; then one barrier says that the next stage
+// has landed and that this one was read; the second half multiplies k 32..63 while it reads
+// the next stage's first operands and copies stage s + P into this one's place.  A copy has
+// P - 1 steps to land, and the matrix cores do not wait for LDS at a step's start.  The copies are inline assembly (tile_dma.h): the compiler cannot tell the
 // stages apart and would wait for all of them before every LDS read.
-#include "bf16_common.h"
+#include "bf16_store.h"
 #include "gemm_common.h"
 #include "tile_dma.h"
 
 namespace moe {
 namespace {
 
-constexpr int kBand = 8;       // row tiles
-
-template <int WR, int WT, int WA, int WB>
+template <int WR, int WT, int WA, int WB, int P, int E>
 struct Tile {
   static constexpr int WAVES = WR * WT;
   static constexpr int A = WR * WA * 16, B = WT * WB * 16;   // rows of the two sides
-  static constexpr int BYTES = (A + B) * 128;                // of a stage
+  static constexpr int LDS = ((P + E) * A + P * B) * 128;
   static constexpr int AD = A / 8 / WAVES, BD = B / 8 / WAVES, DMAS = AD + BD;   // copies (8 rows each) a wave and stage
+  static constexpr int PER_EU = (LDS > 80 * 1024 ? 1 : 2) * WAVES / 4;   // waves a SIMD
+  static_assert(DMAS * P + E * AD <= 63 && E <= 1, "vmcnt");
   static_assert(AD * WAVES * 8 == A && BD * WAVES * 8 == B, "copies");
 };
 
-// 8 values in their own type (float32: two vectors), those past `left` zeros.
-__device__ __forceinline__ void load8_raw(const void* base, size_t i, bool f32, int left, v4u (&r)[2]) {
-  r[0] = r[1] = v4u{0, 0, 0, 0};
-  if (f32) {
-    const uint32_t* q = static_cast<const uint32_t*>(base) + i;
-    if (left >= 8) {
-      r[0] = *reinterpret_cast<const v4u_at4*>(q);
-      r[1] = *reinterpret_cast<const v4u_at4*>(q + 4);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < left) r[j / 4][j % 4] = q[j];
-    }
-  } else {
-    const uint16_t* q = static_cast<const uint16_t*>(base) + i;
-    if (left >= 8) {
-      r[0] = *reinterpret_cast<const v4u_at2*>(q);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < left) r[0][j / 2] |= (uint32_t)q[j] << (j % 2 * 16);
-    }
-  }
-}
-__device__ __forceinline__ float raw_value(const v4u (&r)[2], bool f32, int j) {
-  return f32 ? __uint_as_float(r[j / 4][j % 4]) : bf16_to_f32(r[0][j / 2] >> (j % 2 * 16) & 0xFFFFu);
-}
-
-// The outputs of 16 rows from their sums in `mine` (16 x STRIDE bytes of LDS, the wave's own):
-// 8 neighbouring ones a lane, so that a store covers a whole run of a row.  All loads
-// of the rows' addends go out before the first use; f is applied in a rolled loop, each
-// lane on the values that it stores (unrolled over a tile, its code spilled).
-template <int WA, bool GATED>
-__device__ __forceinline__ void store_rows(const Bf16Args& p, uint8_t* mine, int n, int row0, int end, int lane,
-                                           const v4f (&bias)[2], const v4f (&up_bias)[2]) {
-  constexpr int STRIDE = WA * 64 + 16;
-  constexpr int LPT = WA * (GATED ? 8 : 16) / 8, TPP = kWave / LPT, IT = 16 / TPP;   // lanes a row, rows a pass, passes
-  const int o = lane % LPT * 8;
-  const int left = p.N - n, live = left > 0 ? end - row0 : 0;
-  uint8_t* at = mine + lane / LPT * STRIDE + (GATED ? o / 16 * 32 + o % 16 : o) * 4;
-  v4u add[IT][2];
-  if (p.addend != nullptr) {
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int t = i * TPP + lane / LPT;
-      load8_raw(p.addend, (size_t)(row0 + t) * p.lda + n, p.add_f32, t < live ? left : 0, add[i]);
-    }
-  }
-  if (GATED || p.fn != MOE_FN_NONE || p.bias != nullptr || p.row_scale != nullptr) {
-#pragma unroll 1
-    for (int i = 0; i < IT; ++i) {
-      v4f* q = reinterpret_cast<v4f*>(at + i * TPP * STRIDE);
-      const int t = i * TPP + lane / LPT;
-      const float scale = p.row_scale != nullptr && t < live ? p.row_scale[row0 + t] : 1.0f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v4f v = apply_function(p.fn, q[h] + bias[h]);
-        if constexpr (GATED) v *= q[h + 4] + up_bias[h];
-        q[h] = v * scale;
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int t = i * TPP + lane / LPT;
-    if (t >= live) continue;
-    const v4f* q = reinterpret_cast<const v4f*>(at + i * TPP * STRIDE);
-    v4f v[2] = {q[0], q[1]};
-    if (p.addend != nullptr) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j / 4][j % 4] += raw_value(add[i], p.add_f32, j);
-    }
-    const size_t to = (size_t)(row0 + t) * p.ldo + n;
-    if (p.out_f32) {
-      float* out = static_cast<float*>(p.out) + to;
-      if (left >= 8) {
-        __builtin_nontemporal_store(v[0], reinterpret_cast<v4f_at4*>(out));
-        __builtin_nontemporal_store(v[1], reinterpret_cast<v4f_at4*>(out + 4));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < left) out[j] = v[j / 4][j % 4];
-      }
-    } else {
-      uint16_t* out = static_cast<uint16_t*>(p.out) + to;
-      v4u b;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = pack_bf16(v[j / 2][j % 2 * 2], v[j / 2][j % 2 * 2 + 1]);
-      if (left >= 8) {
-        __builtin_nontemporal_store(b, reinterpret_cast<v4u_at2*>(out));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < left) out[j] = (uint16_t)(b[j / 2] >> (j % 2 * 16));
-      }
-    }
-  }
-}
-
-template <int WR, int WT, int WA, int WB, bool GATED, bool GROUPED>
-__global__ void __launch_bounds__(64 * WR * WT, 2) bf16_tile_kernel(Bf16Args p, int row_tiles, int tok_tiles) {
-  using S = Tile<WR, WT, WA, WB>;
+template <int WR, int WT, int WA, int WB, int P, int E, bool ONCE, bool GATED, bool GROUPED>
+__global__ void __launch_bounds__(64 * WR * WT, (Tile<WR, WT, WA, WB, P, E>::PER_EU)) bf16_tile_kernel(Bf16Args p, int row_tiles, int tok_tiles) {
+  using S = Tile<WR, WT, WA, WB, P, E>;
   constexpr int COLS = GATED ? S::A / 2 : S::A;              // outputs a row
   extern __shared__ __align__(16) uint8_t lds[];
-  int rt, tt;
-  RowTile t;
+  int tok_count = tok_tiles, L;
+  RowTile t = {0, 0, p.T, S::B, 0, 0};
   if constexpr (GROUPED) {
-    const GroupTiles tiles(p, S::B);
-    const int per = (tiles.total * row_tiles + 7) / 8, at = blockIdx.x >> 3, L = (blockIdx.x & 7) * per + at;
-    if (at >= per || L >= tiles.total * row_tiles) return;
-    tt = L / row_tiles;
-    rt = L - tt * row_tiles;
-    t = tiles.find(p, S::B, tt);
+    const GroupTiles<S::B> tiles(p, 1);
+    L = group_item(tiles.total * row_tiles);
+    if (L < 0) return;
+    t = tiles.find(p, L / row_tiles);
+    L -= (L / row_tiles - t.tile) * row_tiles;
+    tok_count = t.tiles;
   } else {
-    // Workgroups are dealt round-robin to the 8 XCDs; each XCD gets a run of the order
-    // below (a band of row tiles, rows of x next), so that the tiles it works on at a
-    // time share their operands in its L2.
-    const int L = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    // Workgroups are dealt round-robin to the 8 XCDs; each XCD gets a run.
+    L = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
     if (L >= row_tiles * tok_tiles) return;
-    const int band = L / (kBand * tok_tiles), width = min(kBand, row_tiles - band * kBand);
-    const int in = L - band * kBand * tok_tiles;
-    tt = in / width;
-    rt = band * kBand + in - tt * width;
-    t = {0, tt * S::B, min(p.T, (tt + 1) * S::B)};
   }
+  // The order (of a group's tiles): a band of row tiles, rows of x next, so that the tiles
+  // an XCD works on at a time share their operands in its L2.
+  const int band = L / (kBand * tok_count), width = min(kBand, row_tiles - band * kBand);
+  const int in = L - band * kBand * tok_count, tt = in / width, rt = band * kBand + in - tt * width;
+  t.first += tt * S::B;
+  t.end = min(t.end, t.first + S::B);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wr = wave % WR, wt = wave / WR;
@@ -192,18 +91,30 @@ __global__ void __launch_bounds__(64 * WR * WT, 2) bf16_tile_kernel(Bf16Args p, 
   }
   const uint32_t lbase = (uint32_t)(uintptr_t)lds;
   // Past the last step the copies read it again, into a place that is not read any more,
-  // so that every step has as many in flight.
-  auto dma = [&](int s, int buf, int i) {
+  // so that every step has as many in flight.  Copy i of step s: first those of x.
+  auto dma_a = [&](int s, int buf, int i) {
     const int from = min(s, steps - 1);
-    const uint32_t o = off[i] + (from == full ? back : 0);
-    const uint32_t to = lbase + buf * S::BYTES + (i < S::AD ? (wave * S::AD + i) * 1024
-                                                            : S::A * 128 + (wave * S::BD + i - S::AD) * 1024);
-    dma16(src[i] + (size_t)from * 128, (int)o, to);
+    const uint32_t o = off[i] + (from == full ? back : 0), to = lbase + buf * (S::A * 128) + (wave * S::AD + i) * 1024;
+    if (ONCE)
+      dma16_once(src[i] + (size_t)from * 128, (int)o, to);
+    else
+      dma16(src[i] + (size_t)from * 128, (int)o, to);
+  };
+  auto dma_b = [&](int s, int buf, int i) {
+    const int from = min(s, steps - 1);
+    const uint32_t o = off[S::AD + i] + (from == full ? back : 0);
+    dma16(src[S::AD + i] + (size_t)from * 128, (int)o,
+          lbase + (P + E) * (S::A * 128) + buf * (S::B * 128) + (wave * S::BD + i) * 1024);
   };
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
+  for (int s = 0; s < P + E; ++s) {
 #pragma unroll
-    for (int i = 0; i < S::DMAS; ++i) dma(s, s, i);
+    for (int i = 0; i < S::AD; ++i) dma_a(s, s, i);
+    if (s < P) {
+#pragma unroll
+      for (int i = 0; i < S::BD; ++i) dma_b(s, s, i);
+    }
+  }
 
   v4f acc[WB][WA];
 #pragma unroll
@@ -212,16 +123,18 @@ __global__ void __launch_bounds__(64 * WR * WT, 2) bf16_tile_kernel(Bf16Args p, 
     for (int r = 0; r < WA; ++r) acc[c][r] = v4f{0.f, 0.f, 0.f, 0.f};
   // The lane's operands: row lane % 16 of a block, piece 4 h + lane / 16 of half h.
   const int at0 = (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) * 16);
-  const int a_at = wr * WA * 2048, b_at = S::A * 128 + wt * WB * 2048;
+  const uint8_t* a_ring = lds + wr * WA * 2048;
+  const uint8_t* b_ring = lds + (P + E) * (S::A * 128) + wt * WB * 2048;
   v4u a[2][WA], b[2][WB];
-  auto read_a = [&](const uint8_t* st, int h, int r) {
-    a[h][r] = *reinterpret_cast<const v4u*>(st + a_at + r * 2048 + (at0 ^ (h * 64)));
+  auto read_a = [&](int buf, int h, int r) {
+    a[h][r] = *reinterpret_cast<const v4u*>(a_ring + buf * (S::A * 128) + r * 2048 + (at0 ^ (h * 64)));
   };
-  auto read_b = [&](const uint8_t* st, int h, int c) {
-    b[h][c] = *reinterpret_cast<const v4u*>(st + b_at + c * 2048 + (at0 ^ (h * 64)));
+  auto read_b = [&](int buf, int h, int c) {
+    b[h][c] = *reinterpret_cast<const v4u*>(b_ring + buf * (S::B * 128) + c * 2048 + (at0 ^ (h * 64)));
   };
-  // Multiplies half H while it reads half 1 - H out of `st` and, with COPY, copies step s.
-  auto half = [&](auto hc, const uint8_t* st, auto copy, int s, int buf) {
+  // Multiplies half H while it reads half 1 - H out of places ra and rb and, with COPY, copies
+  // what step s's places are free for.
+  auto half = [&](auto hc, int ra, int rb, auto copy, int s, int ca, int cb) {
     constexpr int H = decltype(hc)::value, COPY = decltype(copy)::value, N = WA * WB;
     unrolled<N>([&](auto mi) {
       constexpr int m = decltype(mi)::value, c = m / WA, r = m % WA;
@@ -230,36 +143,55 @@ __global__ void __launch_bounds__(64 * WR * WT, 2) bf16_tile_kernel(Bf16Args p, 
         constexpr int i = decltype(ri)::value;
         if constexpr (i * N / (WA + WB) == m) {
           if constexpr (i < WB)
-            read_b(st, 1 - H, i);
+            read_b(rb, 1 - H, i);
           else
-            read_a(st, 1 - H, i - WB);
+            read_a(ra, 1 - H, i - WB);
         }
       });
       if constexpr (COPY)
         unrolled<S::DMAS>([&](auto di) {
           constexpr int i = decltype(di)::value;
-          if constexpr (i * N / S::DMAS == m) dma(s, buf, i);
+          if constexpr (i * N / S::DMAS == m) {
+            if constexpr (i < S::BD)
+              dma_b(s + P, cb, i);
+            else
+              dma_a(s + P + E, ca, i - S::BD);
+          }
         });
       __builtin_amdgcn_sched_barrier(0);
     });
   };
 
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::DMAS) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::DMAS * (P - 1) + E * S::AD) : "memory");
 #pragma unroll
-  for (int c = 0; c < WB; ++c) read_b(lds, 0, c);
+  for (int c = 0; c < WB; ++c) read_b(0, 0, c);
 #pragma unroll
-  for (int r = 0; r < WA; ++r) read_a(lds, 0, r);
-  for (int s = 0; s < full; ++s) {
-    const uint8_t* st = lds + (s & 1) * S::BYTES;
-    half(Int<0>{}, st, Int<0>{}, 0, 0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    half(Int<1>{}, lds + (1 - (s & 1)) * S::BYTES, Int<1>{}, s + 2, s & 1);
+  for (int r = 0; r < WA; ++r) read_a(0, 0, r);
+  int ab = 0, bb = 0;
+  if (!GROUPED || t.first + wt * WB * 16 < t.end) {
+    for (int s = 0; s < full; ++s) {
+      const int an = ab + 1 == P + E ? 0 : ab + 1, bn = bb + 1 == P ? 0 : bb + 1;
+      half(Int<0>{}, ab, bb, Int<0>{}, 0, 0, 0);
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::DMAS * (P - 2) + E * S::AD) : "memory");
+      half(Int<1>{}, an, bn, Int<1>{}, s, ab, bb);
+      ab = an;
+      bb = bn;
+    }
+  } else {
+    // A wave without rows (a group's last tile) copies the weights for the others; the rows
+    // of x that it would copy are its own.
+    for (int s = 0; s < full; ++s) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(S::AD * (P - 2 + E)) : "memory");
+#pragma unroll
+      for (int i = 0; i < S::AD; ++i) dma_a(s + P + E, ab, i);
+      ab = ab + 1 == P + E ? 0 : ab + 1;
+      bb = bb + 1 == P ? 0 : bb + 1;
+    }
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   if (steps > full) {
     // The step that K ends in: pieces past the end are zeros on both sides (the copies
     // read the last piece again in their place).
-    const uint8_t* st = lds + (full & 1) * S::BYTES;
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -267,12 +199,12 @@ __global__ void __launch_bounds__(64 * WR * WT, 2) bf16_tile_kernel(Bf16Args p, 
       const v4u none = {0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < WB; ++c) {
-        read_b(st, h, c);
+        read_b(bb, h, c);
         b[h][c] = in ? b[h][c] : none;
       }
 #pragma unroll
       for (int r = 0; r < WA; ++r) {
-        read_a(st, h, r);
+        read_a(ab, h, r);
         a[h][r] = in ? a[h][r] : none;
       }
 #pragma unroll
@@ -282,63 +214,75 @@ __global__ void __launch_bounds__(64 * WR * WT, 2) bf16_tile_kernel(Bf16Args p, 
     }
   }
 
-  // 16 rows at a time through the wave's part of the stages' place.
+  // The outputs, as many blocks of 16 rows at a time as fit the rings' place.
   __syncthreads();
   constexpr int STRIDE = WA * 64 + 16, OUT = GATED ? WA * 8 : WA * 16;
-  static_assert(S::WAVES * 16 * STRIDE <= 2 * S::BYTES, "staging");
-  uint8_t* mine = lds + wave * 16 * STRIDE;
+  constexpr int FIT = S::LDS / (S::WAVES * 16 * STRIDE), PART = FIT >= WB ? WB : FIT >= WB / 2 ? WB / 2 : WB / 4;
+  static_assert(PART > 0 && WB % PART == 0 && S::WAVES * PART * 16 * STRIDE <= S::LDS, "staging");
+  uint8_t* mine = lds + wave * PART * 16 * STRIDE;
   const int n = rt * COLS + wr * OUT + lane % (OUT / 8) * 8;
-  v4f bias[2] = {}, up_bias[2] = {};
-  if (p.bias != nullptr) {
-    const size_t at = (size_t)t.group * (GATED ? 2 : 1) * p.N + n;
+  v4f bias[2], up_bias[2];
+  load_bias<GATED>(p, t.group, n, bias, up_bias);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      bias[h] = load4_f32(p.bias, at + 4 * h, p.bias_f32, p.N - n - 4 * h);
-      if constexpr (GATED) up_bias[h] = load4_f32(p.bias, at + p.N + 4 * h, p.bias_f32, p.N - n - 4 * h);
+  for (int h = 0; h < WB / PART; ++h) {
+#pragma unroll
+    for (int c = 0; c < PART; ++c)
+#pragma unroll
+      for (int r = 0; r < WA; ++r)
+        *reinterpret_cast<v4f*>(mine + (c * 16 + (lane & 15)) * STRIDE + (r * 16 + (lane >> 4) * 4) * 4) =
+            acc[h * PART + c][r];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int c = 0; c < PART; ++c) {
+      const int row = t.first + (wt * WB + h * PART + c) * 16;
+      if (row >= t.end) break;
+      store_rows<WA, GATED>(p, mine + c * 16 * STRIDE, n, row, t.end, lane, bias, up_bias);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
-  unrolled<WB>([&](auto ci) {
-    constexpr int c = decltype(ci)::value;
-#pragma unroll
-    for (int r = 0; r < WA; ++r)
-      *reinterpret_cast<v4f*>(mine + (lane & 15) * STRIDE + (r * 16 + (lane >> 4) * 4) * 4) = acc[c][r];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    store_rows<WA, GATED>(p, mine, n, t.first + (wt * WB + c) * 16, t.end, lane, bias, up_bias);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  });
 }
 
-template <int WR, int WT, int WA, int WB, bool GATED, bool GROUPED>
+template <int WR, int WT, int WA, int WB, int P, int E, bool ONCE, bool GATED, bool GROUPED>
 hipError_t launch_tile(const Bf16Args& a, hipStream_t stream) {
-  using S = Tile<WR, WT, WA, WB>;
+  using S = Tile<WR, WT, WA, WB, P, E>;
   constexpr int COLS = GATED ? S::A / 2 : S::A;
   const int64_t rt = (a.N + COLS - 1) / COLS;
   const int64_t tt = GROUPED ? a.T / S::B + min(a.E, a.T) : (a.T + S::B - 1) / S::B;
-  auto kern = bf16_tile_kernel<WR, WT, WA, WB, GATED, GROUPED>;
-  constexpr size_t lds = 2 * (size_t)S::BYTES;
+  auto kern = bf16_tile_kernel<WR, WT, WA, WB, P, E, ONCE, GATED, GROUPED>;
+  constexpr size_t lds = (size_t)S::LDS;
   const hipError_t err = raise_lds_limit(reinterpret_cast<const void*>(kern), lds);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(kern, dim3((unsigned)((rt * tt + 7) / 8 * 8)), dim3(64 * S::WAVES), lds, stream, a, (int)rt,
+  const int64_t grid = GROUPED ? group_grid(rt * tt) : (rt * tt + 7) / 8 * 8;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * S::WAVES), lds, stream, a, (int)rt,
                      (int)tt);
   return hipGetLastError();
 }
 
 template <bool GATED, bool GROUPED>
-hipError_t launch_size(const Bf16Args& a, hipStream_t stream) {
-  const int64_t cols = GATED ? 2 * (int64_t)a.N : a.N;
-  const int64_t rows = GROUPED ? (a.T + a.E - 1) / a.E : a.T;
-  const int64_t big = (cols + 255) / 256 * ((rows + 255) / 256) * (GROUPED ? a.E : 1);
-  if (rows > 192 && big >= 256) return launch_tile<2, 4, 8, 4, GATED, GROUPED>(a, stream);
-  return launch_tile<2, 2, 4, 4, GATED, GROUPED>(a, stream);
+hipError_t launch_tile_plan(Bf16Plan plan, const Bf16Args& a, hipStream_t stream) {
+  switch (plan) {
+    case kTile64x64: return launch_tile<1, 4, 4, 1, 4, 0, false, GATED, GROUPED>(a, stream);
+    case kTile128x64: return launch_tile<2, 2, 4, 2, 3, 0, false, GATED, GROUPED>(a, stream);
+    case kTile128x128: return launch_tile<2, 2, 4, 4, 3, 0, false, GATED, GROUPED>(a, stream);
+    case kTile256x128: return launch_tile<4, 2, 4, 4, 3, 0, false, GATED, GROUPED>(a, stream);
+    case kTile256x256: return launch_tile<2, 4, 8, 4, 2, 1, false, GATED, GROUPED>(a, stream);
+    default: break;
+  }
+  if constexpr (GROUPED) {
+    if (plan == kTile128x64Once) return launch_tile<2, 2, 4, 2, 3, 0, true, GATED, GROUPED>(a, stream);
+    if (plan == kTile256x128Once) return launch_tile<4, 2, 4, 4, 3, 0, true, GATED, GROUPED>(a, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_bf16_tile(bool gated, const Bf16Args& a, hipStream_t stream) {
-  if (a.offsets != nullptr) return gated ? launch_size<true, true>(a, stream) : launch_size<false, true>(a, stream);
-  return gated ? launch_size<true, false>(a, stream) : launch_size<false, false>(a, stream);
+hipError_t launch_bf16_tile(Bf16Plan plan, bool gated, const Bf16Args& a, hipStream_t stream) {
+  if (a.offsets != nullptr)
+    return gated ? launch_tile_plan<true, true>(plan, a, stream) : launch_tile_plan<false, true>(plan, a, stream);
+  return gated ? launch_tile_plan<true, false>(plan, a, stream) : launch_tile_plan<false, false>(plan, a, stream);
 }
 
 }  // namespace moe

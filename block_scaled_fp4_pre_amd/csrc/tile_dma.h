@@ -14,6 +14,10 @@ namespace moe {
 __device__ __forceinline__ void dma16(const uint8_t* base, int voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "memory", "m0");
 }
+// The same for bytes that are read once: past the caches as far as they let it.
+__device__ __forceinline__ void dma16_once(const uint8_t* base, int voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(base), "s"(lds) : "memory", "m0");
+}
 __device__ __forceinline__ void dma4(const uint8_t* base, int voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(lds) : "memory", "m0");
 }
