@@ -109,7 +109,7 @@ int moe_w4a4_post_norm(int32_t mma_type, int32_t res_dtype, int32_t w_dtype, int
   if (st != MOE_OK) return st;
   const int act = codes == nullptr ? -1 : mma_type == MOE_MMA_NVF4_X_NVF4 ? 2 : mma_type == MOE_MMA_FP8_X_MXF4 ? 1 : 0;
   const moe::PostNormArgs a = {x, residual, post_weight, gate, next_weight, residual_out, y, codes, scales, rows, cols,
-                               gate_kind, w_dtype == 1, gate_dtype == 1, scale, eps, g};
+                               gate_kind, w_dtype == 1, gate_dtype == 1, scale, g, eps, 1.0 / cols};
   return hip_status(moe::launch_post_norm(act, res_dtype == 1, a, static_cast<hipStream_t>(stream)));
 }
 

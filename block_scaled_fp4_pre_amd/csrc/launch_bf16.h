@@ -120,7 +120,8 @@ struct PostNormArgs {
   int64_t rows;
   int cols, gate_kind;
   bool w_f32, gate_f32;
-  float scale, eps, g;
+  float scale, g;
+  double eps, per_col;   // per_col = 1 / cols
 };
 hipError_t launch_post_norm(int act, bool res_f32, const PostNormArgs& a, hipStream_t stream);
 
