@@ -507,37 +507,32 @@ def _linear_call(cfg_ref, K: int, N: int, mma_type: int, dev: int, prepared: int
 
 
 # ---- bfloat16 operators around the layer ---------------------------------------
-def _rows_of(t, name: str, dtypes, shape, device_index: int) -> int:
+def _rows_of(t, name: str, dtypes, shape, device_index: int):
     """Device address of a matrix whose rows are contiguous and apart (a slice of wider
-    rows, say), as _fits otherwise."""
+    rows, say), and the elements from row to row; as _fits otherwise."""
     p = _fits(t, name, dtypes, shape, device_index, contiguous=False)
+    if t.is_contiguous():
+        return p, shape[1]
     # (a size of one may have any stride)
-    if shape[1] > 1 and t.stride(1) != 1 or shape[0] > 1 and t.stride(0) < shape[1]:
+    stride = t.stride(0) if shape[0] > 1 else shape[1]
+    if shape[1] > 1 and t.stride(1) != 1 or stride < shape[1]:
         raise ValueError(f"{name}: strides {t.stride()}, expected rows of {shape[1]} neighbouring values that do not overlap")
-    return p
+    return p, stride
 
 
-def _row_stride(t) -> int:
-    """Elements from row to row (a single row's stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _product_extras(bias, bias_shape, row_scale, addend, out, dev):
-    """Addresses and codes of what the two products have in common."""
-    T, N = out.shape
-    po = _rows_of(out, "out", _BF16_F32, (T, N), dev)
+def _product_extras(bias, bias_shape, row_scale, addend, shape, dev):
+    """Addresses and codes of what the two products may have besides their operands."""
     pb = pr = pa = None
     bias_dtype = add_dtype = lda = 0
     if bias is not None:
         pb = _fits(bias, "bias", _BF16_F32, bias_shape, dev)
         bias_dtype = 1 if bias.dtype is torch.float32 else 0
     if row_scale is not None:
-        pr = _fits(row_scale, "row_scale", _F32, (T,), dev)
+        pr = _fits(row_scale, "row_scale", _F32, (shape[0],), dev)
     if addend is not None:
-        pa = _rows_of(addend, "addend", _BF16_F32, (T, N), dev)
+        pa, lda = _rows_of(addend, "addend", _BF16_F32, shape, dev)
         add_dtype = 1 if addend.dtype is torch.float32 else 0
-        lda = _row_stride(addend)
-    return bias_dtype, pb, pr, add_dtype, pa, lda, 1 if out.dtype is torch.float32 else 0, po, _row_stride(out)
+    return bias_dtype, pb, pr, add_dtype, pa, lda
 
 
 def moe_w4a4_linear_bf16(x, weight, out, bias=None, function: int = MOE_FN_NONE, gated: bool = False, row_scale=None,
@@ -547,18 +542,21 @@ def moe_w4a4_linear_bf16(x, weight, out, bias=None, function: int = MOE_FN_NONE,
     float32 [N] ([2N]); row_scale float32 [T]; addend bf16 / float32 [T, N] (may be out).
     The rows of x, addend and out may be slices of wider ones."""
     dev = _device_of(out, "out")
-    if x.dim() != 2 or out.dim() != 2:
-        raise ValueError(f"x {tuple(x.shape)} and out {tuple(out.shape)}: expected [T, K] and [T, N]")
-    T, K = x.shape[0], x.shape[1]
-    N = out.shape[1]
-    if out.shape[0] != T:
-        raise ValueError(f"out: {out.shape[0]} rows, expected {T}")
+    shape = out.shape
+    if x.dim() != 2 or len(shape) != 2:
+        raise ValueError(f"x {tuple(x.shape)} and out {tuple(shape)}: expected [T, K] and [T, N]")
+    T, N = shape
+    K = x.shape[1]
     wide = 2 * N if gated else N
-    px = _rows_of(x, "x", _BF16, (T, K), dev)
+    px, ldx = _rows_of(x, "x", _BF16, (T, K), dev)
     pw = _fits(weight, "weight", _BF16, (wide, K), dev)
-    bias_dtype, pb, pr, add_dtype, pa, lda, out_dtype, po, ldo = _product_extras(bias, (wide,), row_scale, addend, out, dev)
-    st = _lib.moe_w4a4_linear_bf16(T, K, N, px, _row_stride(x), pw, function, 1 if gated else 0, bias_dtype, pb, pr,
-                                   add_dtype, pa, lda, out_dtype, po, ldo, _raw_stream(stream, dev))
+    po, ldo = _rows_of(out, "out", _BF16_F32, shape, dev)
+    bias_dtype = add_dtype = lda = 0
+    pb = pr = pa = None
+    if bias is not None or row_scale is not None or addend is not None:
+        bias_dtype, pb, pr, add_dtype, pa, lda = _product_extras(bias, (wide,), row_scale, addend, shape, dev)
+    st = _lib.moe_w4a4_linear_bf16(T, K, N, px, ldx, pw, function, 1 if gated else 0, bias_dtype, pb, pr, add_dtype, pa,
+                                   lda, 1 if out.dtype is torch.float32 else 0, po, ldo, _raw_stream(stream, dev))
     if st != MOE_OK:
         raise MoeError(st, "moe_w4a4_linear_bf16")
 
@@ -583,15 +581,15 @@ def moe_w4a4_grouped_linear_bf16(x, weight, offsets, out, rows=None, row_divisor
                          "expected [T, K], [E, N, K] and [R, N]")
     (Tx, K), (R, N), E = x.shape, out.shape, weight.shape[0]
     wide = 2 * N if gated else N
-    px = _rows_of(x, "x", _BF16, (Tx, K), dev)
+    px, ldx = _rows_of(x, "x", _BF16, (Tx, K), dev)
     pw = _fits(weight, "weight", _BF16, (E, wide, K), dev)
     pf = _fits(offsets, "offsets", _I32, (E + 1,), dev)
     pi = None if rows is None else _fits(rows, "rows", _I32, (R,), dev)
-    bias_dtype, pb, pr, add_dtype, pa, lda, out_dtype, po, ldo = _product_extras(bias, (E, wide), row_scale, addend, out,
-                                                                                 dev)
-    st = _lib.moe_w4a4_grouped_linear_bf16(E, R, K, N, pf, px, Tx, _row_stride(x), pi, row_divisor, pw, function,
-                                           1 if gated else 0, bias_dtype, pb, pr, add_dtype, pa, lda, out_dtype, po, ldo,
-                                           _raw_stream(stream, dev))
+    po, ldo = _rows_of(out, "out", _BF16_F32, (R, N), dev)
+    bias_dtype, pb, pr, add_dtype, pa, lda = _product_extras(bias, (E, wide), row_scale, addend, (R, N), dev)
+    st = _lib.moe_w4a4_grouped_linear_bf16(E, R, K, N, pf, px, Tx, ldx, pi, row_divisor, pw, function,
+                                           1 if gated else 0, bias_dtype, pb, pr, add_dtype, pa, lda,
+                                           1 if out.dtype is torch.float32 else 0, po, ldo, _raw_stream(stream, dev))
     if st != MOE_OK:
         raise MoeError(st, "moe_w4a4_grouped_linear_bf16")
 

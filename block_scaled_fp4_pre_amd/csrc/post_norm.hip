@@ -279,16 +279,19 @@ hipError_t launch_post(const PostNormArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The smallest team that holds the row in at most 4 pieces a thread, as in norm.hip.  Past
-// 16384 values the registers do not hold the row (4 pieces of 1024 threads spilled): 1000 x
-// 32768 106 -> 93 us (float32 stream 140 -> 126), 500 x 65536 with 8 pieces 363 -> 130.
+// Teams of a wave up to 1024 values, of 4 waves up to 4096, of 8 where every row has a CU of
+// its own (1 x 4096 4.4 -> 3.8 us, 64 x 4096 4.9 -> 4.0; 16384 x 4096 128 -> 152) and up to 8192
+// (1 x 8192 6.2 -> 5.0, 8192 x 8192 145 -> 130 against 4 waves of 4 pieces; 16 waves 146).
+// Past 16384 values the registers do not hold the row (4 pieces of 1024 threads spilled):
+// 1000 x 32768 106 -> 93 us (float32 stream 140 -> 126), 500 x 65536 with 8 pieces 363 -> 130.
 template <bool RES_F32, int ACT>
 hipError_t launch_post_act(const PostNormArgs& a, hipStream_t stream) {
   if (a.cols <= 512) return launch_post<RES_F32, ACT, 64, 1>(a, stream);
   if (a.cols <= 1024) return launch_post<RES_F32, ACT, 64, 2>(a, stream);
   if (a.cols <= 2048) return launch_post<RES_F32, ACT, 256, 1>(a, stream);
+  if (a.cols <= 4096 && a.rows <= 256) return launch_post<RES_F32, ACT, 512, 1>(a, stream);
   if (a.cols <= 4096) return launch_post<RES_F32, ACT, 256, 2>(a, stream);
-  if (a.cols <= 8192) return launch_post<RES_F32, ACT, 256, 4>(a, stream);
+  if (a.cols <= 8192) return launch_post<RES_F32, ACT, 512, 2>(a, stream);
   if (a.cols <= 16384) return launch_post<RES_F32, ACT, 1024, 2>(a, stream);
   const int64_t blocks = a.rows < kPostBlocks<kLongThreads> ? a.rows : kPostBlocks<kLongThreads>;
   hipLaunchKernelGGL((post_norm_long_kernel<RES_F32, ACT>), dim3((unsigned)blocks), dim3(kLongThreads), 0, stream, a);

@@ -142,9 +142,10 @@ def test_bindings_refuse_another_device(current_device_0, monkeypatch):  # noqa:
 def test_a_single_rows_stride_says_nothing():
     """A row alone may have any stride, a column too; what the library is told fits both."""
     one = _t((1, 64)).as_strided((1, 64), (3, 1))
-    assert _lib._row_stride(one) == 64
-    assert _lib._row_stride(_t((4, 72))[:, :64]) == 72
-    assert _lib._rows_of(_t((4, 3))[:, :1], "x", (BF,), (4, 1), 0) != 0
+    assert _lib._rows_of(one, "x", (BF,), (1, 64), 0) == (one.data_ptr(), 64)
+    wide = _t((4, 72))
+    assert _lib._rows_of(wide[:, 8:], "x", (BF,), (4, 64), 0) == (wide.data_ptr() + 16, 72)
+    assert _lib._rows_of(_t((4, 3))[:, :1], "x", (BF,), (4, 1), 0)[1] == 3
 
 
 # ---- the objects ---------------------------------------------------------------
