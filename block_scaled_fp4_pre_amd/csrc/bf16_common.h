@@ -118,14 +118,31 @@ __device__ __forceinline__ float silu_f32(float v) {
   return over_one_plus_exp2(v, t, fmaf(u, 1.92596303e-8f, fmaf(u, 1.44269502f, -t)));
 }
 
-// gelu(v) = v erfc(-v / sqrt 2) / 2, the rounding of erfc's argument put back: erfc(x + d) =
-// erfc(x) (1 - h d), h = 2 e^(-x^2) / (sqrt(pi) erfc(x)), which lies between x + sqrt(x^2 + 4/pi)
-// and x + sqrt(x^2 + 2) for x > 0 (and is nothing next to 1 / x below -4).
+// gelu(v) = v F(v), F the normal distribution: F(-a) = t 2^(s + r) for a >= 0 with t = 1 /
+// (1 + 0.3 a), s = -a^2 / 2 log2(e), and r a polynomial of t - 0.6 (a Chebyshev fit of
+// log2(e^(a^2/2) F(-a) / t) over a <= 14.5, within 2^-24) with the roundings of s put back;
+// F(a) = 1 - F(-a).  Far out as in over_one_plus_exp2.  (Through erfcf a 128 x 128 tile's
+// outputs cost as much as 16 steps of its product.)
 __device__ __forceinline__ float gelu_f32(float v) {
 #pragma clang fp contract(off)
-  const float x = v * -0.707106769f, d = fmaf(v, -1.21016175e-8f, fmaf(v, -0.707106769f, -x));
-  const float y = fminf(x, 16.0f), h = y + __builtin_amdgcn_sqrtf(fmaf(y, y, 1.4f));
-  return v * (0.5f * erfcf(x)) * (x < -4.0f ? 1.0f : fmaf(-h, d, 1.0f));
+  const float a = fminf(fabsf(v), 16.0f);
+  const float t = __builtin_amdgcn_rcpf(fmaf(a, 0.3f, 1.0f)), u = t - 0.6f;
+  float r = 0.207756102f;
+  r = fmaf(r, u, -0.20550473f);
+  r = fmaf(r, u, -0.287186265f);
+  r = fmaf(r, u, 0.323197365f);
+  r = fmaf(r, u, 0.318443209f);
+  r = fmaf(r, u, -0.400117517f);
+  r = fmaf(r, u, -0.509796202f);
+  r = fmaf(r, u, 0.537607908f);
+  r = fmaf(r, u, 2.2604425f);
+  r = fmaf(r, u, -1.9513582f);
+  const float h = -0.5f * a, m = h * a, low = fmaf(h, a, -m);          // -a^2 / 2 = m + low
+  const float s = m * 1.44269502f;
+  r += fmaf(low, 1.44269502f, fmaf(m, 1.92596303e-8f, fmaf(m, 1.44269502f, -s)));
+  const bool far = s < -64.0f;
+  const float q = t * (__builtin_amdgcn_exp2f(far ? s + 32.0f : s) * __builtin_amdgcn_exp2f(r));
+  return v < 0.0f ? (far ? v * q * 0x1p-32f : v * q) : v * (1.0f - (far ? 0.0f : q));
 }
 
 // Its tanh form: v (1 + tanh u) / 2 = v / (1 + e^-2u), u = sqrt(2/pi) (v + 0.044715 v^3); the
