@@ -22,41 +22,30 @@ __device__ __forceinline__ v4f mfma_bf16(const v4u& a, const v4u& b, const v4f& 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// A group and its rows; the rows of its tiles, which of them, of how many.
+// A group and its rows; which of its tiles, of how many.
 struct RowTile {
-  int group, first, end, size, tile, tiles;
+  int group, first, end, tile, tiles;
 };
 
-// Rows a tile of a group of n rows has, in units of UNIT: as few tiles as `cap` units each
-// allow, all of them as even as the units are.
-template <int UNIT>
-__host__ __device__ __forceinline__ int tile_rows(int n, int cap) {
-  const int tiles = (n + UNIT * cap - 1) / (UNIT * cap);
-  return tiles <= 1 ? UNIT * cap : (n + UNIT * tiles - 1) / (UNIT * tiles) * UNIT;
-}
-
 // The groups' tiles, in the order of the groups.  Every wave counts them for itself: a
-// lane those of up to 8 consecutive groups, a scan over the lanes says whose a tile is.
-// Offsets are clamped to the rows there are, so that wrong ones give wrong rows but no
-// access outside the tensors.
+// lane those of up to 8 consecutive groups (all their offsets in one trip to memory), a
+// scan over the lanes says whose a tile is.  Offsets are clamped to the rows there are,
+// so that wrong ones give wrong rows but no access outside the tensors.
 template <int UNIT>
 struct GroupTiles {
-  int cap, per, mine, upto, total;
-  __device__ __forceinline__ static int2 rows(const Bf16Args& p, int e) {
-    const int a = min(max(p.offsets[e], 0), p.T), b = min(max(p.offsets[e + 1], 0), p.T);
-    return make_int2(a, max(a, b));
-  }
-  __device__ __forceinline__ GroupTiles(const Bf16Args& p, int units) : cap(units) {
+  static constexpr int PER = 8;                      // 512 groups
+  int per, mine, upto, total, at[PER + 1];
+  __device__ __forceinline__ static int count(int first, int end) { return (max(end - first, 0) + UNIT - 1) / UNIT; }
+  __device__ __forceinline__ explicit GroupTiles(const Bf16Args& p) {
     const int lane = threadIdx.x & (kWave - 1);
     per = (p.E + kWave - 1) / kWave;
+#pragma unroll
+    for (int j = 0; j <= PER; ++j) at[j] = j <= per ? p.offsets[min(lane * per + j, p.E)] : 0;
     mine = 0;
-    for (int j = 0; j < per; ++j) {
-      const int e = lane * per + j;
-      if (e < p.E) {
-        const int2 r = rows(p, e);
-        const int size = tile_rows<UNIT>(r.y - r.x, cap);
-        mine += (r.y - r.x + size - 1) / size;
-      }
+#pragma unroll
+    for (int j = 0; j <= PER; ++j) {
+      at[j] = j <= per ? min(max(at[j], 0), p.T) : at[j - 1];
+      if (j > 0) mine += count(at[j - 1], at[j]);
     }
     upto = mine;
 #pragma unroll
@@ -67,17 +56,22 @@ struct GroupTiles {
     total = __builtin_amdgcn_readlane(upto, kWave - 1);
   }
   // Tile number `tile` < total: its group, the group's rows and tiles, and which of them it is.
-  __device__ __forceinline__ RowTile find(const Bf16Args& p, int tile) const {
+  __device__ __forceinline__ RowTile find(int tile) const {
     const int owner = __builtin_ctzll(__ballot(upto > tile));
-    int left = tile - __builtin_amdgcn_readlane(upto - mine, owner), e = owner * per;
-    for (;; ++e) {
-      const int2 r = rows(p, e);
-      const int size = tile_rows<UNIT>(r.y - r.x, cap);
-      const int n = (r.y - r.x + size - 1) / size;
-      if (left < n) return {e, r.x, r.y, size, left, n};
+    int left = tile - __builtin_amdgcn_readlane(upto - mine, owner);
+    RowTile t = {0, 0, 0, 0, 0};
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int first = __builtin_amdgcn_readlane(at[j], owner), end = __builtin_amdgcn_readlane(at[j + 1], owner);
+      const int n = count(first, end);
+      if (!found && left < n) {
+        t = {owner * per + j, first, end, left, n};
+        found = true;
+      }
       left -= n;
-      if (e + 1 >= p.E) return {e, 0, 1, UNIT * cap, 0, 1};     // (offsets that changed under the kernel)
     }
+    return t;
   }
 };
 

@@ -35,10 +35,10 @@ __global__ void __launch_bounds__(64 * W) bf16_split_kernel(Bf16Args p, int row_
   RowTile t;
   if constexpr (GROUPED) {
     // a group's tiles with the same weights next to each other
-    const GroupTiles<ROWS> tiles(p, 1);
+    const GroupTiles<ROWS> tiles(p);
     const int L = group_item(tiles.total * row_tiles);
     if (L < 0) return;
-    t = tiles.find(p, L / row_tiles);
+    t = tiles.find(L / row_tiles);
     const int in = L - (L / row_tiles - t.tile) * row_tiles;
     rt = in / t.tiles;
     t.first += (in - rt * t.tiles) * ROWS;
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(64 * W) bf16_split_kernel(Bf16Args p, int row_
     if (L >= row_tiles * tok_tiles) return;
     rt = L / tok_tiles;
     const int tt = L - rt * tok_tiles;
-    t = {0, tt * ROWS, min(p.T, (tt + 1) * ROWS), ROWS, 0, 1};
+    t = {0, tt * ROWS, min(p.T, (tt + 1) * ROWS), 0, 1};
   }
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);

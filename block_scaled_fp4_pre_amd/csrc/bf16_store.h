@@ -35,17 +35,18 @@ __device__ __forceinline__ float raw_value(const v4u (&r)[2], bool f32, int j) {
 }
 
 // The outputs of 16 rows from their sums in `mine` (16 x STRIDE bytes of LDS, the wave's own):
-// 8 neighbouring ones a lane, so that a store covers a whole run of a row.  All loads
-// of the rows' addends go out before the first use; f is applied in a rolled loop, each
-// lane on the values that it stores (unrolled over a tile, its code spilled).
+// 8 neighbouring ones a lane, so that a store covers a whole run of a row.  f is applied
+// in a rolled loop, each lane on the values that it stores (unrolled over a tile, its code
+// spilled).  All loads of the rows' addends go out before the first use.  scale: row_scale
+// of row row0 - at + lane (a load for each pass cost 98304 x 2048 x 4096 in groups 5 %).
 template <int WA, bool GATED>
 __device__ __forceinline__ void store_rows(const Bf16Args& p, uint8_t* mine, int n, int row0, int end, int lane,
-                                           const v4f (&bias)[2], const v4f (&up_bias)[2]) {
+                                           const v4f (&bias)[2], const v4f (&up_bias)[2], float scale, int at) {
   constexpr int STRIDE = WA * 64 + 16;
   constexpr int LPT = WA * (GATED ? 8 : 16) / 8, TPP = kWave / LPT, IT = 16 / TPP;   // lanes a row, rows a pass, passes
   const int o = lane % LPT * 8;
   const int left = p.N - n, live = left > 0 ? end - row0 : 0;
-  uint8_t* at = mine + lane / LPT * STRIDE + (GATED ? o / 16 * 32 + o % 16 : o) * 4;
+  uint8_t* place = mine + lane / LPT * STRIDE + (GATED ? o / 16 * 32 + o % 16 : o) * 4;
   v4u add[IT][2];
   if (p.addend != nullptr) {
 #pragma unroll
@@ -54,30 +55,33 @@ __device__ __forceinline__ void store_rows(const Bf16Args& p, uint8_t* mine, int
       load8_raw(p.addend, (size_t)(row0 + t) * p.lda + n, p.add_f32, t < live ? left : 0, add[i]);
     }
   }
-  if (GATED || p.fn != MOE_FN_NONE || p.bias != nullptr || p.row_scale != nullptr) {
+  if (GATED || p.fn != MOE_FN_NONE || p.bias != nullptr) {
 #pragma unroll 1
     for (int i = 0; i < IT; ++i) {
-      v4f* q = reinterpret_cast<v4f*>(at + i * TPP * STRIDE);
-      const int t = i * TPP + lane / LPT;
-      const float scale = p.row_scale != nullptr && t < live ? p.row_scale[row0 + t] : 1.0f;
+      v4f* q = reinterpret_cast<v4f*>(place + i * TPP * STRIDE);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         v4f v = apply_function(p.fn, q[h] + bias[h]);
         if constexpr (GATED) v *= q[h + 4] + up_bias[h];
-        q[h] = v * scale;
+        q[h] = v;
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int t = i * TPP + lane / LPT;
-    if (t >= live) continue;
-    const v4f* q = reinterpret_cast<const v4f*>(at + i * TPP * STRIDE);
+    const v4f* q = reinterpret_cast<const v4f*>(place + i * TPP * STRIDE);
     v4f v[2] = {q[0], q[1]};
+    if (p.row_scale != nullptr) {
+      const float s = __shfl(scale, at + t);
+      v[0] *= s;
+      v[1] *= s;
+    }
     if (p.addend != nullptr) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j / 4][j % 4] += raw_value(add[i], p.add_f32, j);
     }
+    if (t >= live) continue;
     const size_t to = (size_t)(row0 + t) * p.ldo + n;
     if (p.out_f32) {
       float* out = static_cast<float*>(p.out) + to;

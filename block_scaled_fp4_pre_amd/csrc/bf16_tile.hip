@@ -36,12 +36,12 @@ __global__ void __launch_bounds__(64 * WR * WT, (Tile<WR, WT, WA, WB, P, E>::PER
   constexpr int COLS = GATED ? S::A / 2 : S::A;              // outputs a row
   extern __shared__ __align__(16) uint8_t lds[];
   int tok_count = tok_tiles, L;
-  RowTile t = {0, 0, p.T, S::B, 0, 0};
+  RowTile t = {0, 0, p.T, 0, 0};
   if constexpr (GROUPED) {
-    const GroupTiles<S::B> tiles(p, 1);
+    const GroupTiles<S::B> tiles(p);
     L = group_item(tiles.total * row_tiles);
     if (L < 0) return;
-    t = tiles.find(p, L / row_tiles);
+    t = tiles.find(L / row_tiles);
     L -= (L / row_tiles - t.tile) * row_tiles;
     tok_count = t.tiles;
   } else {
@@ -223,8 +223,12 @@ __global__ void __launch_bounds__(64 * WR * WT, (Tile<WR, WT, WA, WB, P, E>::PER
   const int n = rt * COLS + wr * OUT + lane % (OUT / 8) * 8;
   v4f bias[2], up_bias[2];
   load_bias<GATED>(p, t.group, n, bias, up_bias);
+  const int row0 = t.first + wt * WB * 16;
 #pragma unroll
   for (int h = 0; h < WB / PART; ++h) {
+    const int first = row0 + h * PART * 16;
+    float scale = 1.0f;                         // of row first + lane
+    if (p.row_scale != nullptr) scale = p.row_scale[min(first + lane, t.end - 1)];
 #pragma unroll
     for (int c = 0; c < PART; ++c)
 #pragma unroll
@@ -235,9 +239,9 @@ __global__ void __launch_bounds__(64 * WR * WT, (Tile<WR, WT, WA, WB, P, E>::PER
     __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
     for (int c = 0; c < PART; ++c) {
-      const int row = t.first + (wt * WB + h * PART + c) * 16;
+      const int row = first + c * 16;
       if (row >= t.end) break;
-      store_rows<WA, GATED>(p, mine + c * 16 * STRIDE, n, row, t.end, lane, bias, up_bias);
+      store_rows<WA, GATED>(p, mine + c * 16 * STRIDE, n, row, t.end, lane, bias, up_bias, scale, c * 16);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
