@@ -6,12 +6,20 @@
 // operand read spread over the banks (a copy fills places in order: the lane picks the
 // piece instead).
 //
-// A ring of P stages, and the operand registers of half a stage read ahead: a step's first
-// half multiplies k 0..31 while it reads k 32..63; then one barrier says that the next stage
-// has landed and that this one was read; the second half multiplies k 32..63 while it reads
-// the next stage's first operands and copies stage s + P into this one's place.  A copy has
-// P - 1 steps to land, and the matrix cores do not wait for LDS at a step's start.  The copies are inline assembly (tile_dma.h): the compiler cannot tell the
-// stages apart and would wait for all of them before every LDS read.
+// Rings of P stages (P + E of the weights), and the operand registers of half a stage read
+// ahead: a step's first half multiplies k 0..31 while it reads k 32..63; then one barrier
+// says that the next stages have landed and that these were read; the second half multiplies
+// k 32..63 while it reads the next stages' first operands and copies x of step s + P and
+// weights of step s + P + E into these ones' places.  The matrix cores do not wait for LDS
+// at a step's start.  The copies are inline assembly (tile_dma.h): the compiler cannot tell
+// the stages apart and would wait for all of them before every LDS read.
+//
+// 256 x 256 (2 x 4 waves of 128 x 64; 16384 x 4096 x (2 x 2048) gated 400 us, 1.37 PFLOP/s; 8192^3
+// 715 us, 1.54): bound by power, the clock is 1.77 GHz and the MFMAs are busy 75 % of the
+// cycles; LDS is read 1536 and written 512 cycles a step of 2048 MFMA cycles, which is why
+// smaller tiles are slower for each output.  E = 1: 426 -> 409 us, and 1982 -> 1896 for
+// 98304 x 2048 x 4096 in 256 groups, whose weights come from HBM.  64 x 64 (4096 x 4096 x 256 17 us)
+// is bound by the L2s' way to LDS, 31 bytes a cycle and CU.
 #include "bf16_store.h"
 #include "gemm_common.h"
 #include "tile_dma.h"
@@ -31,7 +39,8 @@ struct Tile {
 };
 
 template <int WR, int WT, int WA, int WB, int P, int E, bool ONCE, bool GATED, bool GROUPED>
-__global__ void __launch_bounds__(64 * WR * WT, (Tile<WR, WT, WA, WB, P, E>::PER_EU)) bf16_tile_kernel(Bf16Args p, int row_tiles, int tok_tiles) {
+__global__ void __launch_bounds__(64 * WR * WT, (Tile<WR, WT, WA, WB, P, E>::PER_EU))
+    bf16_tile_kernel(Bf16Args p, int row_tiles, int tok_tiles) {
   using S = Tile<WR, WT, WA, WB, P, E>;
   constexpr int COLS = GATED ? S::A / 2 : S::A;              // outputs a row
   extern __shared__ __align__(16) uint8_t lds[];

@@ -8,6 +8,8 @@
 // pieces of 8 values as in norm.hip, and like there sums, norms and products run in
 // fp64 (hidden behind the loads): h has one rounding, the same whatever the order of
 // the sums, and the codes behind it are reproducible next to the quantizer's borders.
+// 16384 x 4096 with E4M3 codes (472 MB) take 104 us, 4.5 TB/s (91 at a copy's rate): the fp64
+// conversions, 7 a value, are what the loads do not hide (without the first norm 96 us).
 #include "launch_bf16.h"
 #include "moe_w4a4.h"
 #include "norm_rows.h"
