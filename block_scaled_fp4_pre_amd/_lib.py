@@ -625,7 +625,7 @@ def moe_w4a4_experts_bf16(cfg, w1, w2, x, topk_ids, topk_weights, out, workspace
 
 def _gate_kind(gate, rows: int, cols: int) -> int:
     """MOE_GATE_* of a gate by its shape: [cols], [rows, 1] or [rows, cols]."""
-    return MOE_GATE_CHANNEL if gate.dim() == 1 else MOE_GATE_ROW if gate.shape[-1] == 1 else MOE_GATE_FULL
+    return MOE_GATE_CHANNEL if gate.dim() == 1 else MOE_GATE_ROW if gate.shape[-1:] == (1,) else MOE_GATE_FULL
 
 
 def moe_w4a4_post_norm(x, residual, residual_out, eps: float, post_weight=None, gate=None, scale: float = 1.0,

@@ -118,7 +118,7 @@ def test_experts_binding_refuses(current_device_0, change):  # noqa: F811
     dict(residual=_t((4, 64), torch.float16)), dict(residual_out=_t((4, 64), F32)), dict(residual_out=_t((3, 64))),
     dict(post_weight=_t((63,))), dict(post_weight=_t((64,), F32)), dict(next_weight=_t((64,), torch.float16)),
     dict(gate=_t((63,))), dict(gate=_t((1, 64))), dict(gate=_t((4, 2))), dict(gate=_t((3, 1))), dict(gate=_t((4, 64), torch.float16)),
-    dict(gate=_t((4, 1, 1))), dict(gate=_t((4, 1)).expand(4, 64)), dict(y=_t((4, 64), F32)), dict(y=_t((5, 64))),
+    dict(gate=_t((4, 1, 1))), dict(gate=_t(())), dict(gate=_t((4, 1)).expand(4, 64)), dict(y=_t((4, 64), F32)), dict(y=_t((5, 64))),
     dict(codes=None), dict(scales=None), dict(codes=_t((4, 32), U8)), dict(scales=_t((4, 4), U8)),
     dict(mma_type=_lib.MOE_MMA_MXF4_X_MXF4)], ids=lambda c: ",".join(c))
 def test_post_norm_binding_refuses(current_device_0, change):  # noqa: F811
@@ -195,7 +195,7 @@ def _experts_layer():
     dict(shared=_linear16(64, 32)), dict(shared=_linear16(64, 64, 1)), dict(shared=_block_linear(64, 64, 3)),
     dict(shared=_t((64, 64))), dict(post_weight=_t((63,))), dict(post_weight=_t((64,), torch.float16)),
     dict(post_weight=_t((64,)), next_weight=_t((64,), F32)), dict(next_weight=_t((64,), torch.float16)),
-    dict(post_gate=_t((4, 2))), dict(post_gate=_t((3, 1))), dict(post_gate=_t((1, 65))[:, 1:].reshape(64)[:64].view(64)[1:]),
+    dict(post_gate=_t((4, 2))), dict(post_gate=_t((3, 1))), dict(post_gate=_t(())), dict(post_gate=_t((1, 65))[:, 1:].reshape(64)[:64].view(64)[1:]),
     dict(post_gate=_t((4, 64), torch.float16)), dict(post_scale=float("inf")), dict(post_scale=float("nan")),
     dict(post_scale=1.0, out=_t((5, 64))), dict(post_scale=1.0, out=_t((4, 64), torch.int16)),
     dict(x=_t((9, 64)), residual=_t((9, 64)))], ids=lambda c: ",".join(f"{k}{i}" for i, k in enumerate(c)))

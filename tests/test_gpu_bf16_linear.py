@@ -303,6 +303,87 @@ def test_wrong_offsets_and_rows_stay_inside(R, N):
         assert torch.all(buf[:4] == 77.0) and torch.all(buf[4 + R:] == 77.0)
 
 
+# ---- weights past what the caches keep ---------------------------------------------
+def device_product(x, w, gated):
+    """(fp64 values, bound) of x W^T (gated: SwiGLU) by torch's fp64 products on the device;
+    the bound as oracle.bf16_linear.linear's."""
+    x, w = x.double(), w.double()
+    v, err = x @ w.t().contiguous(), (x.shape[1] + 8) * 2.0 ** -23 * (x.abs() @ w.abs().t().contiguous())
+    if not gated:
+        return v, err + 2.0 ** -126
+    n = v.shape[1] // 2
+    f = v[:, :n] * torch.sigmoid(v[:, :n])
+    e = 1.11 * err[:, :n] + f.abs() * 2.0 ** -20 + 2.0 ** -126
+    out = f * v[:, n:]
+    return out, v[:, n:].abs() * e + f.abs() * err[:, n:] + e * err[:, n:] + out.abs() * 2.0 ** -23 + 2.0 ** -126
+
+
+def device_close(got, ref, bound):
+    err, tol = (got.double() - ref).abs(), bound + (ref.abs() + bound) * 2.0 ** -8
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 16, 17, 32, 33, 100])
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+def test_many_weights(T, gated):
+    log(f"[test] linear_bf16 many weights, T {T} gated {gated}")
+    g = torch.Generator(device="cuda").manual_seed(T)
+    K, N = 4168, 8201 if gated else 16401
+    x = torch.randn((T, K), generator=g, device="cuda").to(BF)
+    w = (torch.randn((2 * N if gated else N, K), generator=g, device="cuda") / 64).to(BF)
+    out = torch.full((T + 1, N), 77.0, dtype=BF, device="cuda")
+    _lib.moe_w4a4_linear_bf16(x, w, out[:T], function=FN["silu"] if gated else 0, gated=gated)
+    torch.cuda.synchronize()
+    assert torch.all(out[T] == 77.0)
+    device_close(out[:T], *device_product(x, w, gated))
+
+
+@pytest.mark.parametrize("mean", [0.3, 1.5, 6, 13, 40, 80, 140, 300])
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+def test_many_experts(mean, gated):
+    """Every kernel of the groups, by their mean rows; a hot group and empty ones among them."""
+    log(f"[test] grouped_bf16 many weights, mean {mean} gated {gated}")
+    E, K, N = 48, 1096, 777 if gated else 1411
+    rng = np.random.default_rng(int(10 * mean))
+    counts = rng.poisson(mean, E)
+    counts[5], counts[E - 1] = 0, 0
+    counts[7] = int(4 * mean) + 1
+    R = int(counts.sum())
+    g = torch.Generator(device="cuda").manual_seed(R)
+    x = torch.randn((-(-R // 3), K), generator=g, device="cuda").to(BF)
+    w = (torch.randn((E, 2 * N if gated else N, K), generator=g, device="cuda") / 33).to(BF)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rows = torch.randperm(R, generator=g, device="cuda").to(torch.int32)
+    out = torch.full((R + 1, N), 77.0, dtype=BF, device="cuda")
+    _lib.moe_w4a4_grouped_linear_bf16(x, w, dev(offsets), out[:R], rows=rows, row_divisor=3, function=FN["silu"] if gated else 0,
+                                      gated=gated)
+    torch.cuda.synchronize()
+    assert torch.all(out[R] == 77.0)
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        if a < b:
+            device_close(out[a:b], *device_product(x[(rows[a:b] // 3).long()], w[e], gated))
+
+
+def test_gathered_rows_past_2_gib():
+    """Rows of x more than 2^31 bytes behind its first (which lies as far into its buffer)."""
+    log("[test] grouped_bf16 far gathered rows")
+    K, N, stride = 64, 40, 4096
+    Tx = 500000                                              # 4.1 GB, below 2^31 elements
+    buf = torch.zeros((300000 + Tx, stride), dtype=BF, device="cuda")
+    x = buf[300000:, :K]
+    rng = np.random.default_rng(11)
+    at = np.array([0, 1, 262143, 262144, 262145, 400000, Tx - 1], np.int32)
+    xb, xv = rows_like(rng, len(at), K)
+    x[torch.from_numpy(at.astype(np.int64)).cuda()] = dev_bf16(xb)
+    wb, w = weights(rng, 2, N, K)
+    out = torch.zeros((len(at), N), dtype=BF, device="cuda")
+    _lib.moe_w4a4_grouped_linear_bf16(x, dev_bf16(wb), dev(np.array([0, 3, len(at)], np.int32)), out, rows=dev(at))
+    torch.cuda.synchronize()
+    for a, b, e in ((0, 3, 0), (3, len(at), 1)):
+        close(values(out[a:b]), *bf16_linear.linear(xv[a:b], w[e]), False)
+
+
 # ---- experts ---------------------------------------------------------------------
 def make_experts(rng, H, I, E, k, T):
     (w1b, w1), (w2b, w2) = weights(rng, E, 2 * I, H), weights(rng, E, H, I)

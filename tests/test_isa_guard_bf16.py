@@ -1,5 +1,5 @@
-"""CPU check of the generated gfx950 code of the bfloat16 tile kernel, as
-tests/test_isa_guard_linear.py's for the linear's: its direct-to-LDS copies are inline assembly
+"""CPU check of the generated gfx950 code of the bfloat16 products' kernels, as
+tests/test_isa_guard_linear.py's for the linear's: their direct-to-LDS copies are inline assembly
 counted by vmcnt waits, sound only while the compiler uses neither M0 nor vector
 memory of its own between the first copy and the drain, and while nothing spills."""
 import os
@@ -11,24 +11,28 @@ import pytest
 from tests.test_isa_guard import CSRC, ROOT, _hipcc, _split_asm
 
 
-@pytest.fixture(scope="module")
-def kernels(tmp_path_factory):
+FLAGS = {"bf16_tile": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "bf16_split": []}
+
+
+@pytest.fixture(scope="module", params=FLAGS)
+def kernels(request, tmp_path_factory):
     hipcc = _hipcc()
     if hipcc is None:
         pytest.skip("hipcc not available")
-    out = tmp_path_factory.mktemp("isa") / "bf16_tile.s"
+    name = request.param
+    out = tmp_path_factory.mktemp("isa") / f"{name}.s"
     cmd = [hipcc, "-O3", "-std=c++17", "-I", os.path.join(ROOT, "include"), "--offload-arch=gfx950",
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form",
-           "--cuda-device-only", "-S", "-o", str(out), os.path.join(CSRC, "bf16_tile.hip")]
+           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", *FLAGS[name],
+           "--cuda-device-only", "-S", "-o", str(out), os.path.join(CSRC, f"{name}.hip")]
     r = subprocess.run(cmd, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     text = out.read_text()
     found = {}
-    for m in re.finditer(r"^(_ZN3moe\w*bf16_tile_kernel\w*):(?:\s*;.*)?$", text, re.M):
+    for m in re.finditer(rf"^(_ZN3moe\w*{name}_kernel\w*):(?:\s*;.*)?$", text, re.M):
         found[m.group(1)] = text[m.end():text.find(".section", m.end())]
-    scratch = dict(re.findall(r"\.name:\s+(_ZN3moe\w*bf16_tile_kernel\w*)\n(?:.*\n)*?\s+\.private_segment_fixed_size:\s+(\d+)",
+    scratch = dict(re.findall(rf"\.name:\s+(_ZN3moe\w*{name}_kernel\w*)\n(?:.*\n)*?\s+\.private_segment_fixed_size:\s+(\d+)",
                               text))
-    assert found, "no tile kernels in the assembly"
+    assert found, "no kernels in the assembly"
     return found, scratch
 
 
