@@ -48,7 +48,7 @@ enum Bf16Plan {
 //   64     -            -            -            1986 (1093)  1545 (881)   1634 (875)   1700 (927)
 //   96     -            -            -            2566 (1424)  1623 (914)   1709 (914)   1764 (947)
 //   128    -            -            -            3242 (1790)  2102 (1098)  1792 (938)   1815 (971)
-//   192    -            -            -            -            2679 (1323)  2219 (1229)  2084 (1115)
+//   192    -            -            -            -            2680 (1323)  2219 (1229)  2084 (1115)
 inline bool bf16_once(const Bf16Args& a, bool gated, int64_t groups) {
   return groups * a.N * a.K * (gated ? 4 : 2) >= (int64_t)128 << 20;
 }
