@@ -119,11 +119,14 @@ __device__ __forceinline__ double lanes_sum(double v) {
 
 // 1 / sqrt(v): the instruction's estimate and three steps of Newton's, to the last bits
 // of fp64 (a division by a square root takes every wave about 600 cycles more, twice a row).
+// Of infinity 0, as a division has it: a step would make 0 * infinity of it, and a row's finite
+// values NaN.
 __device__ __forceinline__ double inverse_root(double v) {
-  double y = __builtin_amdgcn_rsq(v);
+  const double estimate = __builtin_amdgcn_rsq(v);
+  double y = estimate;
 #pragma unroll
   for (int i = 0; i < 3; ++i) y = fma(0.5 * y, fma(-v * y, y, 1.0), y);
-  return y;
+  return estimate == 0.0 ? 0.0 : y;
 }
 
 // The row's factor before its norm: scale, and a gate of rows.

@@ -193,6 +193,31 @@ def test_no_rows():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("cols", [512, 2048, 4096, 16384, 32768])
+@pytest.mark.parametrize("res_f32", [False, True])
+def test_infinity_in_a_row(cols, res_f32):
+    """x / sqrt(mean x^2) with an infinity in the row: 0 for the finite values, whose stream
+    stays as it is, and NaN in its own place; an infinity in the stream does the same to y.
+    Exact: nothing is rounded."""
+    log(f"[test] post norm of rows with an infinity, cols {cols} float32 stream {res_f32}")
+    rng = np.random.default_rng(cols)
+    xd, rd = typed(rng.normal(size=(4, cols)), False)[0], typed(rng.normal(size=(4, cols)), res_f32)[0]
+    xd[1, 5], xd[2, cols - 1] = float("inf"), float("-inf")
+    w = torch.ones(cols, device="cuda")
+    at = torch.zeros((4, cols), dtype=torch.bool, device="cuda")
+    at[1, 5] = at[2, cols - 1] = True
+    ro = torch.empty_like(rd)
+    _lib.moe_w4a4_post_norm(xd, rd, ro, EPS, post_weight=w)
+    torch.cuda.synchronize()
+    assert torch.equal(torch.isnan(ro), at)
+    assert torch.equal(ro[1:3][~at[1:3]], rd[1:3][~at[1:3]])
+    y = torch.empty_like(xd)
+    _lib.moe_w4a4_post_norm(xd, rd, ro, EPS, next_weight=w, y=y)
+    torch.cuda.synchronize()
+    assert torch.equal(ro[at], xd[at].to(ro.dtype)) and not torch.any(torch.isinf(ro[~at]))
+    assert torch.equal(torch.isnan(y), at) and torch.all(y[1:3][~at[1:3]] == 0) and torch.all(torch.isfinite(y[::3]))
+
+
 # ---- the block that ends with it ---------------------------------------------------
 H, I, E, K = 512, 256, 16, 3
 ROUTE = dict(scoring=_lib.MOE_SCORE_SQRTSOFTPLUS, num_groups=4, topk_groups=2, renormalize=True, scale=1.5)
