@@ -83,15 +83,20 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const uint16_t
   }
 }
 
+// A launch takes fewer than 2^32 threads: 2^23 tokens at a time.
+constexpr int kCombineTokens = 1 << 23;
+
 hipError_t launch_combine(const uint16_t* y, const int32_t* pos, const float* w, int T, int H, int k,
                           uint16_t* out, hipStream_t stream) {
-  if (T <= 0) return hipSuccess;
   // Two pieces per thread once a row has at least 512 of them (H >= 4096).
-  if (H / 8 >= 2 * kCombineThreads)
-    hipLaunchKernelGGL(combine_kernel<2>, dim3(T), dim3(kCombineThreads), 0, stream, y, pos, w, H, k, out);
-  else
-    hipLaunchKernelGGL(combine_kernel<1>, dim3(T), dim3(kCombineThreads), 0, stream, y, pos, w, H, k, out);
-  return hipGetLastError();
+  const auto kern = H / 8 >= 2 * kCombineThreads ? combine_kernel<2> : combine_kernel<1>;
+  for (int64_t t = 0; t < T; t += kCombineTokens) {
+    const int n = T - t < kCombineTokens ? (int)(T - t) : kCombineTokens;
+    hipLaunchKernelGGL(kern, dim3(n), dim3(kCombineThreads), 0, stream, y, pos + t * k, w + t * k, H, k, out + t * H);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe
