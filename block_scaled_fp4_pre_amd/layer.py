@@ -53,6 +53,10 @@ class _Block:
         """The routed experts of y (or of the codes _codes gave) into out, on the current stream."""
         raise NotImplementedError
 
+    def _held(self):
+        """The layer's own tensors that `_experts` refuses as its output."""
+        return ()
+
     def _check_block(self, T, gate, bias, scoring, num_groups, topk_groups, scale, shared, residual_out, out,
                      post=(None, None, None, None), x=None) -> None:
         """Everything that the steps behind the norm would refuse: the norm may
@@ -90,8 +94,10 @@ class _Block:
                 place = _lib._fits(post_gate, "post_gate", types, ((H,), (T, 1), (T, H))[kind - 1], dev)
                 if place % 16 and kind != _lib.MOE_GATE_ROW:
                     raise ValueError("post_gate: not 16-byte aligned")
-                if T > 0 and place in [t.data_ptr() for t in (residual_out, out) if t is not None]:
-                    raise ValueError("post_gate: in the place of an output")
+            places = [t.data_ptr() for t in (residual_out, out) if t is not None and T > 0]
+            for name, t in (("post_weight", post_weight), ("post_gate", post_gate), ("next_weight", next_weight)):
+                if t is not None and t.data_ptr() in places:
+                    raise ValueError(f"{name}: in the place of an output")
             if post_scale is not None and not abs(post_scale) <= 3.402823466e38:
                 raise ValueError(f"post_scale: {post_scale}")
         if out is not None:
@@ -106,6 +112,9 @@ class _Block:
                 raise ValueError("out: in the place of residual_out")
             if after and x is not None and place == x.data_ptr() and T > 0:
                 raise ValueError("out: in the place of x, the residual stream")
+            for t in (*self._held(), *(shared._held() if shared is not None else ())):
+                if t is not None and place == t.data_ptr() and T > 0:
+                    raise ValueError("out: in the place of weights or a workspace")
 
     def forward_block(self, x, residual, norm_weight, eps, gate_weight, residual_out=None, bias=None,
                       scoring=_lib.MOE_SCORE_SOFTMAX, num_groups=1, topk_groups=1, renormalize=True, scale=1.0,
@@ -361,6 +370,10 @@ class W4A4Linear:
         return W4A4Linear(self.K, self.N, max_tokens, self.device,
                           self.mma_type if mma_type is None else mma_type, prepared=self.prepared)
 
+    def _held(self):
+        """Its own tensors that may not be its output."""
+        return self.prepared, self.workspace
+
     def load_canonical(self, codes, scales) -> None:
         """codes uint8 [N, K/2] and scales uint8 [N, K/32], MXFP4 (moe_w4a4_quantize)."""
         with torch.cuda.device(self.device):
@@ -424,6 +437,10 @@ class Bf16Linear:
             _lib._fits(bias, "bias", (torch.bfloat16, torch.float32), (wide,), self.device.index)
         self.weight, self.bias, self.function, self.gated = weight, bias, function, gated
 
+    def _held(self):
+        """Its own tensors that may not be its output."""
+        return self.weight, self.bias
+
     def forward(self, x, out=None, addend=None, row_scale=None, dtype=torch.bfloat16, stream=None):
         """x bf16 [T, K] -> out [T, N] (bf16 or float32; made of `dtype` if None):
         (addend +) (row_scale *) f(x W^T + bias); addend [T, N] may be out."""
@@ -443,6 +460,9 @@ class Bf16MLP:
         if gate_up.N != down.K or gate_up.device != down.device:
             raise ValueError(f"down: from {down.K} on {down.device}, expected {gate_up.N} on {gate_up.device}")
         self.gate_up, self.down, self.K, self.N, self.device = gate_up, down, gate_up.K, down.N, down.device
+
+    def _held(self):
+        return self.down._held()
 
     def forward(self, x, out=None, addend=None, row_scale=None, dtype=torch.bfloat16, stream=None):
         """x bf16 [T, K] -> out [T, N], the rest for the down projection (Bf16Linear.forward)."""
@@ -483,6 +503,10 @@ class Bf16Experts(_Block):
             _lib.moe_w4a4_experts_bf16(self.cfg, self.w1, self.w2, x, topk_ids, topk_weights, out, self.workspace,
                                        stream=stream)
         return out
+
+    # ---- the steps of forward_block ------------------------------------------
+    def _held(self):
+        return self.w1, self.w2, self.workspace
 
     def _experts(self, T, y, codes, ids, weights, out) -> None:
         _lib.moe_w4a4_experts_bf16(self.cfg, self.w1, self.w2, y, ids, weights, out, self.workspace)
