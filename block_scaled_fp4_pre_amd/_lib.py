@@ -29,6 +29,7 @@ MOE_MEGA_HCOUNT_WORD = 816        # first per-expert h count of that region (wor
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_SQRTSOFTPLUS = 0, 1, 2
 MOE_FN_NONE, MOE_FN_RELU, MOE_FN_SILU, MOE_FN_GELU, MOE_FN_GELU_TANH = range(5)
 MOE_BF16_MAX_ROWS = 1 << 24      # tokens that the bfloat16 products take
+MOE_BF16_MAX_OUT = 1 << 36       # and tokens times out_features
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_ROW, MOE_GATE_FULL = range(4)
 
 # Every symbol include/moe_w4a4.h declares.

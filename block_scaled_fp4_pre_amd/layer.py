@@ -71,8 +71,11 @@ class _Block:
                 raise ValueError(f"{name}: from {lin.K} to {lin.N} on {lin.device}, expected {H} to {n} on {self.device}")
             if isinstance(lin, W4A4Linear) and lin.max_tokens < T:
                 raise ValueError(f"{name}: holds {lin.max_tokens} tokens, not {T}")
-            if not isinstance(lin, W4A4Linear) and T > _lib.MOE_BF16_MAX_ROWS:
-                raise ValueError(f"{name}: takes {_lib.MOE_BF16_MAX_ROWS} tokens, not {T}")
+            if not isinstance(lin, W4A4Linear):
+                widest = max(lin.gate_up.N, lin.N) if isinstance(lin, Bf16MLP) else lin.N
+                most = min(_lib.MOE_BF16_MAX_ROWS, _lib.MOE_BF16_MAX_OUT // widest)
+                if T > most:
+                    raise ValueError(f"{name}: takes {most} tokens, not {T}")
         if not isinstance(gate, (W4A4Linear, Bf16Linear)):
             _lib._fits(gate, "gate_weight", (torch.bfloat16,), (E, H), dev, contiguous=False)
         if shared is not None and not isinstance(shared, (W4A4Linear, Bf16Linear, Bf16MLP)):

@@ -56,3 +56,14 @@ def test_out_in_the_place_of_weights(no_norm):
 
 def down_of(down):
     return Bf16MLP(Bf16Linear(_t((256, 64)), gated=True), down)
+
+
+def test_more_tokens_than_the_shared_mlp_takes(no_norm):
+    """2^36 values between its two products at most: 2^20 tokens of 65536."""
+    layer, T = experts_layer(), (1 << 20) + 1
+    layer.max_tokens = 1 << 21
+    mlp = Bf16MLP(Bf16Linear(_t((1 << 16, 64))), Bf16Linear(_t((64, 1 << 16))))
+    x = _t((T, 64))
+    args = {**BLOCK, "x": x, "residual": x}
+    with pytest.raises(ValueError, match=f"takes {1 << 20} tokens"):
+        layer.forward_block(**args, shared=mlp)
