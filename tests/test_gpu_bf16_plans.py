@@ -12,7 +12,7 @@ import torch
 from block_scaled_fp4_pre_amd import _lib
 from tests.bf16_plans import CASES, IDS, largest, offsets, whole
 from tests.gpu_support import dev, log
-from tests.test_gpu_bf16_linear import FN
+from tests.test_gpu_bf16_linear import FN, SIZES
 
 pytestmark = pytest.mark.gpu
 
@@ -98,6 +98,13 @@ def test_sums(case):
     sums_exact(case)
     if case[2]:
         sums_exact(case, gather=3)
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("T,K,N", SIZES)
+def test_sums_of_more_sizes(T, K, N, gated):
+    log(f"[test] bf16 sums T {T} K {K} N {N} gated {gated}")
+    sums_exact(("", gated, 0, T, K, N))
 
 
 @pytest.mark.parametrize("case", CASES, ids=IDS)
