@@ -32,12 +32,21 @@ enum Bf16Plan {
   kSplit16x8Once, kSplit32x16Once, kSplit32x32Once,
   kTile64x64, kTile128x64, kTile128x128, kTile256x128, kTile256x256, kTile128x64Once, kTile256x128Once
 };
-// Weights too many to be left in the caches (256 MB) from call to call, and few rows for
-// each: the time is the weights' way from HBM.  Read once, past the caches, they come at 6.9-7.0
-// TB/s instead of 6.1-6.3 (48 rows of 256 experts, 4096 to 2 x 2048: 214 against 240 us; 8
-// x 4096 x 32000: 45 against 51), but 33 MB that the caches hold come slower (8 x 4096 to 2 x
-// 2048: 8.4 against 7.6 us).  Measured by the mean rows of a group, 256 groups, us, 4096 to 2 x
-// 2048 (2048 to 4096):
+// 128 MiB of weights and more, and few rows for each: the time is the weights' way from HBM.
+// Read once, past the caches, they come at 6.9-7.0 TB/s instead of 6.1-6.3 (48 rows of 256
+// experts, 4096 to 2 x 2048: 214 against 240 us).  The caches hold 256 MB: a call repeated on weights
+// of up to that is faster through them, one whose weights others have pushed out is slower.  us
+// through the caches / past them, repeated; then behind a pass that writes 1 GiB:
+//   8 x 4096 x 8000 (63 MiB, left to the caches)   11.5 / 11.2    27 / 16
+//   8 x 4096 x 16300 (127 MiB, left to them)       20.5 / 26      62 / 32
+//   8 x 4096 x 16500 (129 MiB, past them)          22 / 28-31     66 / 34
+//   8 x 4096 x 24000 (188 MiB, past them)          29 / 32        70 / 36
+//   8 x 4096 x 32000 (250 MiB, past them)          38 / 46       106 / 49
+// (8 x 4096 to 2 x 2048, 33 MB, repeated: 7.6 / 8.4.)  Groups count as far as the rows go, whatever
+// the offsets say (the host does not see them), and their rows are taken to be alike: 512 rows of 256
+// experts, 4096 to 2 x 2048, take 1243 us where each has two, and 242 where one has all, whose weights
+// 64 tiles of rows read each for themselves (128 x 64 once: 1401 and 47).  Measured by the mean
+// rows of a group, 256 groups, us, 4096 to 2 x 2048 (2048 to 4096):
 //   rows   16 x 8       32 x 16      32 x 32      128 x 64     256 x 128    256 x 128    256 x 256
 //          split once   split once   split once   tile once    tile once    tile         tile
 //   4      1320 (673)   1235 (631)   1261 (707)   1365 (700)   1390 (735)   1502 (778)   1591 (817)
@@ -60,7 +69,8 @@ inline bool bf16_once(const Bf16Args& a, bool gated, int64_t groups) {
 // 4096 x 4096 128 x 128 32.6, 128 x 64 40; 2048 x 4096 x 4096 256 x 128 55, 128 x 128 58, 256 x 256 71;
 // 4096 x 2048 x 4096 256 x 256 57, 256 x 128 63; 4096 x 4096 x 256 64 x 64 17.1, 128 x 64 21.7, 32 x 64
 // 41.7; 4096 x 256 x 4096 256 x 256 15.7, 256 x 128 17.2, 128 x 64 21.9; 1000 x 64 x 1000 64 x 64 4.2, 128 x
-// 64 4.8, 32 x 32 5.5; 37 groups, 1517 rows, 1000 to 777, 64 x 64 22.2, 128 x 64 20.4, 128 x 128 27.0.
+// 64 4.8, 32 x 32 5.5; 37 groups, 1517 rows, 1000 to 777, 64 x 64 18.6, 128 x 64 20.8, 128 x 128 26.1, 32 x 64 33.
+// (The products of K = 4096 had their weights in the caches, as a repeated call has.)
 struct Bf16Tile {
   Bf16Plan plan;
   int w, t;              // weight rows, rows of x
@@ -98,8 +108,10 @@ inline Bf16Plan bf16_plan(bool gated, const Bf16Args& a) {
       best = c.plan;
     }
   }
-  // One token tile of few weight rows: 8 waves a tile take its K in half the steps (1 x 4096 x 256
-  // 4.1 against 4.5 us, 8 x 4096 x 2048 4.9 against 5.7, 1 x 4096 x 4096 7.3 against 7.1).
+  // Few weight rows: 8 waves a tile take its K in half the steps (1 x 4096 x 256 4.1 against 4.5 us, 8 x
+  // 4096 x 2048 4.9 against 5.7, 1 x 4096 x 4096 7.3 against 7.1).  Nothing else is asked: groups of a row
+  // each take them too, 16 of 4096 to 512 in the same time (12.6 us), 64 of 512 to 256 7.9 against 7.1, 512 of
+  // 8 to 256 76 against 41.
   if (best == kSplit16x8 && cols <= 16 * 192) return kSplit16x8Wide;
   return best;
 }

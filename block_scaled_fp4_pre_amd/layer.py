@@ -133,7 +133,8 @@ class _Block:
         (the norm of out under post_weight), and y' = the norm of h' under next_weight,
         what the next block reads (None without one), both norms with eps.
         x bf16 [T, H]; residual bf16 / float32 [T, H] (residual_out like it,
-        may be it; a new tensor if None), or None (h is x then); norm_weight [H].
+        may be it; a new tensor if None), or None (h is x then, and residual_out
+        None); norm_weight [H].
         gate_weight: bf16 [E, H], whose logits are torch's own product and so
         rounded to bf16 before the choice; or a W4A4Linear or Bf16Linear with
         out_features E, whose logits are float32.  bias float32 [E].

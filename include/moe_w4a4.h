@@ -427,7 +427,7 @@ enum { MOE_FN_NONE = 0, MOE_FN_RELU = 1, MOE_FN_SILU = 2, MOE_FN_GELU = 3, MOE_F
  * the address of one).  Supported: K % 8 == 0, 8 <= K <= 65536, 1 <= N <= 2^20,
  * num_tokens <= 2^24, num_tokens * N <= 2^36, strides <= 2^22; 0 tokens enqueue nothing
  * and look at no pointer.  Sums, bias, f, scale and addend are fp32, with one rounding
- * to out; f is within 2^-20 of its value (an output below 2^-126 within 2^-126).  The
+ * to out; f is within 2^-20 of its value (a value below 2^-126 within 2^-126).  The
  * order of a sum is fixed by the sizes: the result is deterministic, sums of another
  * num_tokens may be ordered otherwise.  A row's non-finite values stay in its outputs.
  * No workspace: calls may run at the same time. */
